@@ -4,7 +4,7 @@ import subprocess
 import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-SOURCES = ["csrc/okls_api.cpp", "csrc/okls_kernels.hip"]
+SOURCES = ["csrc/okls_api.cpp", "csrc/okls_kernels.hip", "csrc/linear_api.cpp", "csrc/linear_kernels.hip"]
 OUT = os.path.join(HERE, "libokls.so")
 
 

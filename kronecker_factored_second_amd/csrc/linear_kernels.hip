@@ -1,0 +1,570 @@
+// gfx950 kernels of the 8-bit linear-layer operators (okls_linear.h).
+//
+//  quantize_kernel   a 128 x 128 tile of x in registers, its 8-bit form along
+//                    the rows, along the columns, or both from the one read.
+//  rms_norm_kernel   residual addition, fp64 mean square, 8-bit output.
+//  norm_grad_kernel  dx and partial sums of dweight; norm_dw_kernel joins them.
+//  matmul kernels    c = a b^T on v_mfma_scale_f32_16x16x128_f8f6f4, whose
+//                    E8M0 operand scales apply the block scales for free.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/okls_linear.h"
+#include "linear_kernels.h"
+
+namespace okls {
+namespace {
+
+typedef _Float16 half_t;
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef int intx4 __attribute__((ext_vector_type(4)));
+typedef int intx8 __attribute__((ext_vector_type(8)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+
+struct bf16_t { uint16_t bits; };
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16_t v) { return __uint_as_float(static_cast<uint32_t>(v.bits) << 16); }
+__device__ __forceinline__ float to_f32(half_t v) { return static_cast<float>(v); }
+
+// round to nearest even; a NaN keeps its sign and becomes quiet
+__device__ __forceinline__ uint16_t bf16_bits(float f) {
+  const uint32_t u = __float_as_uint(f);
+  if ((u & 0x7fffffffu) > 0x7f800000u) return static_cast<uint16_t>((u >> 16) | 0x40u);
+  return static_cast<uint16_t>((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+}
+template <typename T> __device__ __forceinline__ T from_f32(float f);
+template <> __device__ __forceinline__ float from_f32<float>(float f) { return f; }
+template <> __device__ __forceinline__ bf16_t from_f32<bf16_t>(float f) { return bf16_t{bf16_bits(f)}; }
+template <> __device__ __forceinline__ half_t from_f32<half_t>(float f) { return static_cast<half_t>(f); }
+
+// one element of a tensor whose type is known at run time (weights, outputs at an edge)
+__device__ __forceinline__ float load_any(const void* p, int64_t i, int dtype) {
+  if (dtype == OKLS_F32) return static_cast<const float*>(p)[i];
+  if (dtype == OKLS_BF16) return to_f32(static_cast<const bf16_t*>(p)[i]);
+  return to_f32(static_cast<const half_t*>(p)[i]);
+}
+__device__ __forceinline__ void store_any(void* p, int64_t i, int dtype, float v) {
+  if (dtype == OKLS_F32) static_cast<float*>(p)[i] = v;
+  else if (dtype == OKLS_BF16) static_cast<bf16_t*>(p)[i] = from_f32<bf16_t>(v);
+  else static_cast<half_t*>(p)[i] = from_f32<half_t>(v);
+}
+
+// Eight consecutive elements as fp32; the first n of them (n <= 8) exist, the
+// others are zero.  vec: p is 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load8(float (&v)[8], const T* p, int n, bool vec) {
+  if (n >= 8 && vec) {
+    if constexpr (sizeof(T) == 4) {
+      const floatx4 a = reinterpret_cast<const floatx4*>(p)[0], b = reinterpret_cast<const floatx4*>(p)[1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+    } else {
+      const u16x8 a = *reinterpret_cast<const u16x8*>(p);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (__is_same(T, bf16_t)) v[j] = to_f32(bf16_t{a[j]});
+        else v[j] = to_f32(__builtin_bit_cast(half_t, static_cast<uint16_t>(a[j])));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? to_f32(p[j]) : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8], int n, bool vec) {
+  if (n >= 8 && vec) {
+    if constexpr (sizeof(T) == 4) {
+      reinterpret_cast<floatx4*>(p)[0] = floatx4{v[0], v[1], v[2], v[3]};
+      reinterpret_cast<floatx4*>(p)[1] = floatx4{v[4], v[5], v[6], v[7]};
+    } else {
+      u16x8 a;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = __builtin_bit_cast(uint16_t, from_f32<T>(v[j]));
+      *reinterpret_cast<u16x8*>(p) = a;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = from_f32<T>(v[j]);
+  }
+}
+__device__ __forceinline__ void load8_any(float (&v)[8], const void* p, int64_t i, int n, int dtype) {
+  if (dtype == OKLS_F32) {
+    const float* q = static_cast<const float*>(p) + i;
+    load8(v, q, n, (reinterpret_cast<uintptr_t>(q) & 15) == 0);
+  } else if (dtype == OKLS_BF16) {
+    const bf16_t* q = static_cast<const bf16_t*>(p) + i;
+    load8(v, q, n, (reinterpret_cast<uintptr_t>(q) & 15) == 0);
+  } else {
+    const half_t* q = static_cast<const half_t*>(p) + i;
+    load8(v, q, n, (reinterpret_cast<uintptr_t>(q) & 15) == 0);
+  }
+}
+
+__device__ __forceinline__ int clamp8(int64_t left) { return left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0; }
+
+// ---------------------------------------------------------------------------
+// The 8-bit form
+// ---------------------------------------------------------------------------
+
+// |v| as the bits of its float, 0 for NaN and infinities: non-negative floats
+// order as their bits do, so the block maximum is an integer maximum
+__device__ __forceinline__ uint32_t finite_abs(float v) {
+  const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
+  return u >= 0x7f800000u ? 0u : u;
+}
+// The scale byte e + 127 of a block whose largest finite |v| has the bits
+// `top`: F = 1.75 2^T (T = 8 for e4m3, 15 for e5m2), so e is top's exponent
+// less T, and one more where its significand is above 1.75.  Subnormals have
+// exponent field 0 and clamp with the small normal numbers at byte 0.
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+  constexpr int T = FMT == OKLS_E4M3 ? 8 : 15;
+  const int b = static_cast<int>(top >> 23) - T + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return top == 0 ? 127u : static_cast<uint32_t>(b > 0 ? b : 0);
+}
+// 2^-e: byte is at most 247, so the field 254 - byte is a normal number's
+__device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  int r = 0;
+  if constexpr (FMT == OKLS_E4M3) {
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+  } else {
+    r = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, r, false);
+    r = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, r, true);
+  }
+  return static_cast<uint32_t>(r);
+}
+template <int FMT>
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
+  return uint2{codes4<FMT>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+               codes4<FMT>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+}
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// One 128 x 128 tile per pass, 256 threads: thread t holds rows 8 (t / 16) + p
+// and columns 8 (t % 16) + j.  A row's maximum is over 16 neighbouring lanes, a
+// column's over the four lane groups of a wave and, through LDS, the four
+// waves.  The transposed codes go through LDS so that they leave as whole rows
+// of 128 bytes.
+constexpr int kTileStride = 128 + 16;   // bytes; 16-byte rows that start at different banks
+
+template <typename T, int FMT>
+__global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
+  __shared__ uint32_t col_top[4][128];
+  __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kTileStride];
+  const int t = threadIdx.x, c8 = t & 15, rg = t >> 4, wave = t >> 6;
+  const int64_t tiles_c = (a.cols + 127) >> 7, n_tiles = tiles_c * ((a.rows + 127) >> 7);
+  const T* x = static_cast<const T*>(a.x);
+  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (a.ldx * sizeof(T)) % 16 == 0;
+  for (int64_t it = blockIdx.x; it < n_tiles; it += gridDim.x) {
+    const int64_t br = it / tiles_c, bc = it - br * tiles_c;
+    const int64_t r0 = br * 128 + rg * 8, c0 = bc * 128 + c8 * 8;
+    const int nc = clamp8(a.cols - c0);
+    float v[8][8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      if (r0 + p < a.rows) load8(v[p], x + (r0 + p) * a.ldx + c0, nc, vec);
+      else
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[p][j] = 0.0f;
+    }
+    if (a.row_factor != nullptr) {
+      float cf[8];
+      load8_any(cf, a.col_factor, c0, nc, a.col_dtype);
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const float rf = r0 + p < a.rows ? a.row_factor[r0 + p] : 0.0f;
+        // no value past the matrix's end, where 0 times a factor's infinity or NaN would not be 0
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[p][j] = j < nc && r0 + p < a.rows ? v[p][j] * rf * cf[j] : 0.0f;
+      }
+    }
+    if (a.along_cols.codes != nullptr) {
+      const Blocked& o = a.along_cols;
+      uint64_t bytes = 0;
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max_u32(top, finite_abs(v[p][j]));
+#pragma unroll
+        for (int m = 1; m < 16; m <<= 1) top = max_u32(top, __shfl_xor(top, m, 64));
+        const uint32_t byte = scale_byte<FMT>(top);
+        bytes |= static_cast<uint64_t>(byte) << (8 * p);
+        if (r0 + p < a.rows)
+          *reinterpret_cast<uint2*>(o.codes + (r0 + p) * o.ld + c0) = codes8<FMT>(v[p], scale_inverse(byte));
+      }
+      // rows past the end have the scale of zeros; the row stride is padded to 16
+      if (c8 == 0 && r0 < o.ld_scale && r0 < ((a.rows + 15) & ~int64_t(15)))
+        *reinterpret_cast<uint64_t*>(o.scales + bc * o.ld_scale + r0) = bytes;
+    }
+    if (a.along_rows.codes != nullptr) {
+      const Blocked& o = a.along_rows;
+      uint32_t top[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        top[j] = 0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) top[j] = max_u32(top[j], finite_abs(v[p][j]));
+        top[j] = max_u32(top[j], __shfl_xor(top[j], 16, 64));
+        top[j] = max_u32(top[j], __shfl_xor(top[j], 32, 64));
+      }
+      if ((t & 63) < 16)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) col_top[wave][c8 * 8 + j] = top[j];
+      __syncthreads();
+      uint64_t bytes = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = max_u32(m, col_top[w][c8 * 8 + j]);
+        const uint32_t byte = scale_byte<FMT>(m);
+        bytes |= static_cast<uint64_t>(byte) << (8 * j);
+        float u[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) u[p] = v[p][j];
+        *reinterpret_cast<uint2*>(tile + (c8 * 8 + j) * kTileStride + rg * 8) = codes8<FMT>(u, scale_inverse(byte));
+      }
+      if (rg == 0 && c0 < ((a.cols + 15) & ~int64_t(15)))
+        *reinterpret_cast<uint64_t*>(o.scales + br * o.ld_scale + c0) = bytes;
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = q * 32 + (t >> 3), chunk = t & 7;
+        if (bc * 128 + col < a.cols)
+          *reinterpret_cast<uint4*>(o.codes + (bc * 128 + col) * o.ld + br * 128 + chunk * 16) =
+              *reinterpret_cast<const uint4*>(tile + col * kTileStride + chunk * 16);
+      }
+      __syncthreads();   // the next tile writes both LDS arrays
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Norm
+// ---------------------------------------------------------------------------
+
+// the sum of v over the block's four waves, in every thread, in a fixed order
+template <typename V>
+__device__ __forceinline__ V block_sum(V v, V* sh) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = sh[0] + sh[1] + sh[2] + sh[3];
+  __syncthreads();
+  return v;
+}
+
+template <typename T, int FMT>
+__global__ __launch_bounds__(256) void rms_norm_kernel(NormArgs a) {
+  __shared__ double sh[4];
+  const int t = threadIdx.x;
+  const T* x = static_cast<const T*>(a.x);
+  const T* res = static_cast<const T*>(a.residual);
+  T* hs = static_cast<T*>(a.h);
+  auto al = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * sizeof(T)) % 16 == 0; };
+  const bool vx = al(x, a.ldx), vr = al(res, a.ldr), vh = al(hs, a.ldh);
+  const int64_t chunks = ((a.cols + 127) >> 7) * 16;   // whole blocks: past the end v = 0
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    auto value = [&](float (&v)[8], int64_t c, bool first) {
+      const int n = clamp8(a.cols - c * 8);
+      load8(v, x + row * a.ldx + c * 8, n, vx);
+      if (res != nullptr) {
+        float r[8];
+        load8(r, res + row * a.ldr + c * 8, n, vr);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = to_f32(from_f32<T>(v[j] + r[j]));
+        if (first) store8(hs + row * a.ldh + c * 8, v, n, vh);
+      }
+      return n;
+    };
+    double ss = 0.0;
+    for (int64_t c = t; c < chunks; c += 256) {
+      float v[8];
+      value(v, c, true);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), ss);
+    }
+    ss = block_sum(ss, sh);
+    const float rstd = static_cast<float>(1.0 / sqrt(ss / static_cast<double>(a.cols) + static_cast<double>(a.eps)));
+    if (t == 0) a.rstd[row] = rstd;
+    for (int64_t c = t; c < chunks; c += 256) {
+      float v[8], w[8];
+      const int n = value(v, c, false);
+      load8_any(w, a.weight, c * 8, n, a.weight_dtype);
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = j < n ? v[j] * rstd * w[j] : 0.0f;
+        top = max_u32(top, finite_abs(v[j]));
+      }
+#pragma unroll
+      for (int m = 1; m < 16; m <<= 1) top = max_u32(top, __shfl_xor(top, m, 64));
+      const uint32_t byte = scale_byte<FMT>(top);
+      *reinterpret_cast<uint2*>(a.out.codes + row * a.out.ld + c * 8) = codes8<FMT>(v, scale_inverse(byte));
+      if ((t & 15) == 0) a.out.scales[(c >> 4) * a.out.ld_scale + row] = static_cast<uint8_t>(byte);
+    }
+  }
+}
+
+constexpr int kGradBlocks = 512;   // most blocks of a launch, each with one row of partial sums of dweight
+
+template <typename T>
+__global__ __launch_bounds__(256) void norm_grad_kernel(NormGradArgs a) {
+  __shared__ float sh[4];
+  const int t = threadIdx.x;
+  const T* dy = static_cast<const T*>(a.dy);
+  const T* h = static_cast<const T*>(a.h);
+  const T* dh = static_cast<const T*>(a.dh);
+  T* dx = static_cast<T*>(a.dx);
+  auto al = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * sizeof(T)) % 16 == 0; };
+  const bool vy = al(dy, a.lddy), vh = al(h, a.ldh), vd = al(dh, a.lddh), vx = al(dx, a.lddx);
+  const int64_t chunks = (a.cols + 7) >> 3;
+  float* part = a.ws + blockIdx.x * (chunks * 8);
+  for (int64_t c = t; c < chunks; c += 256)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[c * 8 + j] = 0.0f;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const float rstd = a.rstd[row];
+    float dot = 0.0f;
+    for (int64_t c = t; c < chunks; c += 256) {
+      const int n = clamp8(a.cols - c * 8);
+      float g[8], u[8], w[8];
+      load8(g, dy + row * a.lddy + c * 8, n, vy);
+      load8(u, h + row * a.ldh + c * 8, n, vh);
+      load8_any(w, a.weight, c * 8, n, a.weight_dtype);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) dot = fmaf(g[j] * w[j], u[j] * rstd, dot);
+    }
+    const float mean = block_sum(dot, sh) / static_cast<float>(a.cols);
+    for (int64_t c = t; c < chunks; c += 256) {
+      const int n = clamp8(a.cols - c * 8);
+      float g[8], u[8], w[8], d[8];
+      load8(g, dy + row * a.lddy + c * 8, n, vy);
+      load8(u, h + row * a.ldh + c * 8, n, vh);
+      load8_any(w, a.weight, c * 8, n, a.weight_dtype);
+      if (dh != nullptr) load8(d, dh + row * a.lddh + c * 8, n, vd);
+      else
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float hat = u[j] * rstd;
+        part[c * 8 + j] = fmaf(g[j], hat, part[c * 8 + j]);
+        u[j] = fmaf(rstd, g[j] * w[j] - hat * mean, d[j]);
+      }
+      store8(dx + row * a.lddx + c * 8, u, n, vx);
+    }
+  }
+}
+
+// dweight[c] = the partial sums of column c, added in fp64 in the blocks' order
+__global__ __launch_bounds__(256) void norm_dw_kernel(const float* part, int n_parts, int64_t stride, int64_t cols, void* dweight, int dtype) {
+  __shared__ double sh[4][64];
+  const int c = threadIdx.x & 63, g = threadIdx.x >> 6;
+  for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * 64; c0 < cols; c0 += static_cast<int64_t>(gridDim.x) * 64) {
+    double s = 0.0;
+    if (c0 + c < cols)
+      for (int p = g; p < n_parts; p += 4) s += static_cast<double>(part[p * stride + c0 + c]);
+    sh[g][c] = s;
+    __syncthreads();
+    if (g == 0 && c0 + c < cols) store_any(dweight, c0 + c, dtype, static_cast<float>(sh[0][c] + sh[1][c] + sh[2][c] + sh[3][c]));
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Product
+// ---------------------------------------------------------------------------
+
+// Two ways to multiply.  The 8-bit matrix instruction runs at twice the rate
+// of the 16-bit ones and applies the E8M0 scales itself, but it lines up each
+// eight consecutive products on the largest of them and cuts what is below
+// 2^-13 of it before the fp32 addition (measured on this card, the same in the
+// unscaled instruction): about 1.6e-5 of a result in norm.  That is far below
+// a 16-bit result's own rounding (1.7e-3 in bf16, 2e-4 in fp16), so 16-bit
+// results take it; fp32 results, which go into the optimizer's factors, would
+// lose nine bits.  They convert codes times scale to bf16, which holds every
+// such value exactly (4 significant bits; a value below 2^-126, subnormal in
+// fp32, may count as zero), and take the bf16 instruction, whose sums round as
+// fp32's.
+
+// cbsz / blgp of the f8f6f4 instructions: 0 e4m3, 1 e5m2 (the okls_code values)
+template <int FP, int FQ>
+__device__ __forceinline__ floatx4 mfma8(const intx8& p, const intx8& q, const floatx4& c, int sp, int sq) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, c, FP, FQ, 0, sp, 0, sq);
+}
+
+__device__ __forceinline__ intx8 frag(const uint8_t* p) {
+  const intx4 lo = reinterpret_cast<const intx4*>(p)[0], hi = reinterpret_cast<const intx4*>(p)[1];
+  return intx8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
+
+// codes 8 s .. 8 s + 7 of a lane's 32, times 2^(byte - 127), in bf16
+template <int F>
+__device__ __forceinline__ bf16x8 widen(const intx8& f, int s, int byte) {
+  const float scale = __uint_as_float(static_cast<uint32_t>(byte) << 23);
+  bf16x8 r;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const unsigned w = static_cast<unsigned>(f[2 * s + q]);
+    bf16x2 lo, hi;
+    if constexpr (F == OKLS_E4M3) {
+      lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false);
+      hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true);
+    } else {
+      lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, false);
+      hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, true);
+    }
+    r[4 * q] = lo[0], r[4 * q + 1] = lo[1], r[4 * q + 2] = hi[0], r[4 * q + 3] = hi[1];
+  }
+  return r;
+}
+
+// One 16 x 16 block of c per wave straight from global memory.  Rows of b are
+// the first operand, so a lane ends with four consecutive columns of one row
+// of c: lane l holds c[l % 16][4 (l / 16) + e].
+template <int FA, int FB, bool F32>
+__global__ __launch_bounds__(256) void matmul_direct_kernel(MatmulArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t m = a.a.rows, n = a.b.rows, blocks = (a.a.cols + 127) >> 7;
+  const int64_t tiles_n = (n + 15) >> 4, tile = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t tm = tile / tiles_n, tn = tile - tm * tiles_n;
+  if (tm * 16 >= m) return;
+  // rows past the end read the last one; what they give is not stored
+  const int64_t ra = tm * 16 + (lane & 15) < m ? tm * 16 + (lane & 15) : m - 1;
+  const int64_t rb = tn * 16 + (lane & 15) < n ? tn * 16 + (lane & 15) : n - 1;
+  const uint8_t* pa = a.a.codes + ra * a.a.ld + (lane >> 4) * 32;
+  const uint8_t* pb = a.b.codes + rb * a.b.ld + (lane >> 4) * 32;
+  floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t k = 0; k < blocks; ++k) {
+    const int sa = a.a.scales[k * a.a.ld_scale + ra], sb = a.b.scales[k * a.b.ld_scale + rb];
+    const intx8 fa = frag(pa + k * 128), fb = frag(pb + k * 128);
+    if constexpr (F32) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen<FB>(fb, s, sb), widen<FA>(fa, s, sa), acc, 0, 0, 0);
+    } else {
+      acc = mfma8<FB, FA>(fb, fa, acc, sb, sa);
+    }
+  }
+  const int64_t row = tm * 16 + (lane & 15), col = tn * 16 + (lane >> 4) * 4;
+  if (row >= m) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (col + e < n) {
+      const int64_t i = row * a.ldc + col + e;
+      store_any(a.c, i, a.c_dtype, a.accumulate ? acc[e] + load_any(a.c, i, a.c_dtype) : acc[e]);
+    }
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(void* c, int dtype, int64_t m, int64_t n, int64_t ldc) {
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < m * n; i += gridDim.x * 256ll) store_any(c, i / n * ldc + i % n, dtype, 0.0f);
+}
+
+// calls go(a's format, b's format, fp32 result) with compile-time values
+template <class F>
+void by_format(const MatmulArgs& a, F go) {
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  auto second = [&](auto fa) {
+    auto third = [&](auto fb) {
+      if (a.c_dtype == OKLS_F32) go(fa, fb, std::true_type{});
+      else go(fa, fb, std::false_type{});
+    };
+    if (a.b.format == OKLS_E4M3) third(I0{});
+    else third(I1{});
+  };
+  if (a.a.format == OKLS_E4M3) second(I0{});
+  else second(I1{});
+}
+
+int blocks_up_to(int64_t n, int most) { return static_cast<int>(n < most ? n : most); }
+
+}  // namespace
+
+hipError_t launch_quantize(const QuantArgs& a, hipStream_t s) {
+  const int64_t tiles = ((a.rows + 127) / 128) * ((a.cols + 127) / 128);
+  const int grid = blocks_up_to(tiles, 1 << 20);
+  // the two outputs may differ in format only by two launches
+  auto go = [&](const QuantArgs& q, int fmt) {
+    if (fmt == OKLS_E4M3) {
+      if (q.x_dtype == OKLS_F32) quantize_kernel<float, OKLS_E4M3><<<grid, 256, 0, s>>>(q);
+      else if (q.x_dtype == OKLS_BF16) quantize_kernel<bf16_t, OKLS_E4M3><<<grid, 256, 0, s>>>(q);
+      else quantize_kernel<half_t, OKLS_E4M3><<<grid, 256, 0, s>>>(q);
+    } else {
+      if (q.x_dtype == OKLS_F32) quantize_kernel<float, OKLS_E5M2><<<grid, 256, 0, s>>>(q);
+      else if (q.x_dtype == OKLS_BF16) quantize_kernel<bf16_t, OKLS_E5M2><<<grid, 256, 0, s>>>(q);
+      else quantize_kernel<half_t, OKLS_E5M2><<<grid, 256, 0, s>>>(q);
+    }
+  };
+  if (a.along_cols.codes != nullptr && a.along_rows.codes != nullptr && a.along_cols.format != a.along_rows.format) {
+    QuantArgs one = a, two = a;
+    one.along_rows = Blocked{};
+    two.along_cols = Blocked{};
+    go(one, a.along_cols.format);
+    go(two, a.along_rows.format);
+  } else {
+    go(a, a.along_cols.codes != nullptr ? a.along_cols.format : a.along_rows.format);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+  const int grid = blocks_up_to(a.rows, 1 << 20);
+  if (a.out.format == OKLS_E4M3) {
+    if (a.dtype == OKLS_F32) rms_norm_kernel<float, OKLS_E4M3><<<grid, 256, 0, s>>>(a);
+    else if (a.dtype == OKLS_BF16) rms_norm_kernel<bf16_t, OKLS_E4M3><<<grid, 256, 0, s>>>(a);
+    else rms_norm_kernel<half_t, OKLS_E4M3><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (a.dtype == OKLS_F32) rms_norm_kernel<float, OKLS_E5M2><<<grid, 256, 0, s>>>(a);
+    else if (a.dtype == OKLS_BF16) rms_norm_kernel<bf16_t, OKLS_E5M2><<<grid, 256, 0, s>>>(a);
+    else rms_norm_kernel<half_t, OKLS_E5M2><<<grid, 256, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+size_t norm_grad_workspace(int64_t rows, int64_t cols) {
+  return static_cast<size_t>(blocks_up_to(rows, kGradBlocks)) * ((cols + 7) / 8 * 8) * 4;
+}
+
+hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s) {
+  const int grid = blocks_up_to(a.rows, kGradBlocks);
+  if (grid > 0) {
+    if (a.dtype == OKLS_F32) norm_grad_kernel<float><<<grid, 256, 0, s>>>(a);
+    else if (a.dtype == OKLS_BF16) norm_grad_kernel<bf16_t><<<grid, 256, 0, s>>>(a);
+    else norm_grad_kernel<half_t><<<grid, 256, 0, s>>>(a);
+  }
+  norm_dw_kernel<<<blocks_up_to((a.cols + 63) / 64, 1 << 16), 256, 0, s>>>(a.ws, grid, (a.cols + 7) / 8 * 8, a.cols, a.dweight, a.weight_dtype);
+  return hipGetLastError();
+}
+
+size_t matmul_workspace(int64_t, int64_t, int64_t) { return 0; }
+
+hipError_t launch_matmul(const MatmulArgs& a, hipStream_t s) {
+  const int64_t m = a.a.rows, n = a.b.rows;
+  if (a.a.cols == 0) {
+    if (!a.accumulate) zero_kernel<<<blocks_up_to((m * n + 255) / 256, 4096), 256, 0, s>>>(a.c, a.c_dtype, m, n, a.ldc);
+    return hipGetLastError();
+  }
+  const unsigned grid = static_cast<unsigned>((((m + 15) / 16) * ((n + 15) / 16) + 3) / 4);
+  by_format(a, [&](auto fa, auto fb, auto f32) {
+    matmul_direct_kernel<decltype(fa)::value, decltype(fb)::value, decltype(f32)::value><<<grid, 256, 0, s>>>(a);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace okls
