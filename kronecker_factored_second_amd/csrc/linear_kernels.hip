@@ -4,8 +4,10 @@
 //                    the rows, along the columns, or both from the one read.
 //  rms_norm_kernel   residual addition, fp64 mean square, 8-bit output.
 //  norm_grad_kernel  dx and partial sums of dweight; norm_dw_kernel joins them.
-//  matmul kernels    c = a b^T on v_mfma_scale_f32_16x16x128_f8f6f4, whose
-//                    E8M0 operand scales apply the block scales for free.
+//  matmul kernels    c = a b^T on the scaled 8-bit matrix instructions, whose
+//                    E8M0 operand scales apply the block scales for free, or
+//                    on bf16 ones: tiles through LDS (matmul_tile_kernel), or
+//                    straight from memory for few rows (matmul_few_kernel).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -22,6 +24,7 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef int intx4 __attribute__((ext_vector_type(4)));
 typedef int intx8 __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
@@ -404,9 +407,14 @@ __global__ __launch_bounds__(256) void norm_dw_kernel(const float* part, int n_p
 // fp32's.
 
 // cbsz / blgp of the f8f6f4 instructions: 0 e4m3, 1 e5m2 (the okls_code values)
-template <int FP, int FQ>
-__device__ __forceinline__ floatx4 mfma8(const intx8& p, const intx8& q, const floatx4& c, int sp, int sq) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, c, FP, FQ, 0, sp, 0, sq);
+
+// f(integral_constant 0), ..., f(integral_constant N - 1)
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void for_each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    for_each<N, I + 1>(f);
+  }
 }
 
 __device__ __forceinline__ intx8 frag(const uint8_t* p) {
@@ -414,9 +422,9 @@ __device__ __forceinline__ intx8 frag(const uint8_t* p) {
   return intx8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 
-// codes 8 s .. 8 s + 7 of a lane's 32, times 2^(byte - 127), in bf16
-template <int F>
-__device__ __forceinline__ bf16x8 widen(const intx8& f, int s, int byte) {
+// codes 8 s .. 8 s + 7 of a lane's, times 2^(byte - 127), in bf16
+template <int F, class V>
+__device__ __forceinline__ bf16x8 widen(const V& f, int s, int byte) {
   const float scale = __uint_as_float(static_cast<uint32_t>(byte) << 23);
   bf16x8 r;
 #pragma unroll
@@ -435,40 +443,368 @@ __device__ __forceinline__ bf16x8 widen(const intx8& f, int s, int byte) {
   return r;
 }
 
-// One 16 x 16 block of c per wave straight from global memory.  Rows of b are
-// the first operand, so a lane ends with four consecutive columns of one row
-// of c: lane l holds c[l % 16][4 (l / 16) + e].
-template <int FA, int FB, bool F32>
-__global__ __launch_bounds__(256) void matmul_direct_kernel(MatmulArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t m = a.a.rows, n = a.b.rows, blocks = (a.a.cols + 127) >> 7;
-  const int64_t tiles_n = (n + 15) >> 4, tile = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int64_t tm = tile / tiles_n, tn = tile - tm * tiles_n;
-  if (tm * 16 >= m) return;
-  // rows past the end read the last one; what they give is not stored
-  const int64_t ra = tm * 16 + (lane & 15) < m ? tm * 16 + (lane & 15) : m - 1;
-  const int64_t rb = tn * 16 + (lane & 15) < n ? tn * 16 + (lane & 15) : n - 1;
-  const uint8_t* pa = a.a.codes + ra * a.a.ld + (lane >> 4) * 32;
-  const uint8_t* pb = a.b.codes + rb * a.b.ld + (lane >> 4) * 32;
-  floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t k = 0; k < blocks; ++k) {
-    const int sa = a.a.scales[k * a.a.ld_scale + ra], sb = a.b.scales[k * a.b.ld_scale + rb];
-    const intx8 fa = frag(pa + k * 128), fb = frag(pb + k * 128);
+// waits for all but the newest v vector-memory operations, other counters untouched
+#define WAIT_VM(v) __builtin_amdgcn_s_waitcnt(((v) & 15) | (7 << 4) | (15 << 8) | (((v) >> 4) << 14))
+#define WAIT_LDS() __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14))
+
+// c[row][col .. col + N) = v (+ c), the first n of them
+template <int N>
+__device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int64_t col, float (&v)[N], bool vec) {
+  const int64_t i = row * a.ldc + col, left = a.b.rows - col;
+  if (vec && left >= N) {
+    auto put = [&](auto* c) {
+#pragma unroll
+      for (int q = 0; q < N; q += 8) {
+        float u[8], w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = v[q + e];
+        if (a.accumulate) {
+          load8(w, c + i + q, 8, true);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] += w[e];
+        }
+        store8(c + i + q, u, 8, true);
+      }
+    };
+    if (a.c_dtype == OKLS_F32) put(static_cast<float*>(a.c));
+    else if (a.c_dtype == OKLS_BF16) put(static_cast<bf16_t*>(a.c));
+    else put(static_cast<half_t*>(a.c));
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e < left) store_any(a.c, i + e, a.c_dtype, a.accumulate ? v[e] + load_any(a.c, i + e, a.c_dtype) : v[e]);
+  }
+}
+
+// A tile of c per workgroup.  The wave's region is GI x GJ blocks of 32 x 32;
+// lane r of block row i holds row r GI + i of it, so that a lane's scale bytes
+// of all its block rows are neighbours: one load each side per 128 of k.
+template <int WM_, int WN_, int GI_, int GJ_>
+struct Tile {
+  static constexpr int WM = WM_, WN = WN_, GI = GI_, GJ = GJ_;
+  static constexpr int NW = WM * WN, NT = NW * 64, RM = 32 * GI, RN = 32 * GJ, BM = WM * RM, BN = WN * RN;
+  static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;   // 1 KB copies per wave and stage
+};
+using TileBig = Tile<2, 4, 4, 2>;     // 256 x 256, 8 waves
+using TileSmall = Tile<2, 2, 2, 2>;   // 128 x 128, 4 waves, two workgroups a CU
+
+struct MatmulPlan {
+  int big;         // which tile
+  int splits;      // of the summed axis
+  int64_t tm, tn;  // tiles
+};
+
+template <int N> struct ScaleWord { using type = uint32_t; };
+template <> struct ScaleWord<2> { using type = uint16_t; };
+
+template <class C, int FA, int FB, bool F32>
+__global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, MatmulPlan plan) {
+  constexpr int GI = C::GI, GJ = C::GJ;
+  constexpr int P = F32 ? 4 : 2;          // phases of a stage of 128 of k
+  constexpr int FW = 16 / P;              // dwords of a lane's codes in a block row and phase
+  __shared__ __attribute__((aligned(16))) uint8_t sA0[C::BM * 128], sA1[C::BM * 128], sB0[C::BN * 128], sB1[C::BN * 128];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int64_t m = a.a.rows, n = a.b.rows;
+
+  // workgroup w runs on XCD w % 8; each XCD takes a run of neighbouring tiles
+  // (all splits of it) in bands of 8 tile rows, so that the 32 it holds at a
+  // time share operand rows in its L2
+  const int64_t per = plan.tm * plan.tn;
+  const int64_t total = per * plan.splits, w = blockIdx.x, x = w & 7;
+  const int64_t id = x * (total >> 3) + (x < (total & 7) ? x : (total & 7)) + (w >> 3);
+  const int64_t split = id / per, t = id - split * per;
+  const int64_t band = t / (8 * plan.tn), in = t - band * 8 * plan.tn;
+  const int64_t high = plan.tm - band * 8 < 8 ? plan.tm - band * 8 : 8;
+  const int64_t m0 = (band * 8 + in % high) * C::BM, n0 = in / high * C::BN;
+
+  const int64_t blocks = (a.a.cols + 127) >> 7;
+  const int64_t k0 = blocks * split / plan.splits;
+  const int nst = static_cast<int>(blocks * (split + 1) / plan.splits - k0);
+
+  // copies: 8 rows of 128 bytes each; 16-byte chunk c of row r lies at
+  // position c ^ (r / GI % 8), so that the 16-byte reads of consecutive lanes
+  // (rows GI apart) go to different banks.  Rows past the end read the last
+  // one; what they give is not stored.
+  const uint8_t *ga[C::LA], *gb[C::LB];
+#pragma unroll
+  for (int q = 0; q < C::LA; ++q) {
+    const int row = 8 * (wave + C::NW * q) + (lane >> 3);
+    const int64_t r = m0 + row < m ? m0 + row : m - 1;
+    ga[q] = a.a.codes + r * a.a.ld + k0 * 128 + (((lane & 7) ^ (row / GI & 7)) << 4);
+  }
+#pragma unroll
+  for (int q = 0; q < C::LB; ++q) {
+    const int row = 8 * (wave + C::NW * q) + (lane >> 3);
+    const int64_t r = n0 + row < n ? n0 + row : n - 1;
+    gb[q] = a.b.codes + r * a.b.ld + k0 * 128 + (((lane & 7) ^ (row / GJ & 7)) << 4);
+  }
+  auto copy = [&](int st, uint8_t* dA, uint8_t* dB) {
+    const int64_t at = static_cast<int64_t>(st) * 128;
+#pragma unroll
+    for (int q = 0; q < C::LA; ++q)
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(ga[q] + at),
+                                       (__attribute__((address_space(3))) void*)(dA + (wave + C::NW * q) * 1024), 16, 0, 0);
+#pragma unroll
+    for (int q = 0; q < C::LB; ++q)
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(gb[q] + at),
+                                       (__attribute__((address_space(3))) void*)(dB + (wave + C::NW * q) * 1024), 16, 0, 0);
+  };
+  // scale bytes of this lane's block rows; rows padded to 16 exist
+  const int r32 = lane & 31, half = lane >> 5;
+  using WA = typename ScaleWord<GI>::type;
+  using WB = typename ScaleWord<GJ>::type;
+  const int64_t ra = m0 + wm * C::RM + r32 * GI, rb = n0 + wn * C::RN + r32 * GJ;
+  const int64_t ma = ((m + 15) & ~int64_t(15)) - GI, mb = ((n + 15) & ~int64_t(15)) - GJ;
+  const uint8_t* pa = a.a.scales + k0 * a.a.ld_scale + (ra < ma ? ra : ma);
+  const uint8_t* pb = a.b.scales + k0 * a.b.ld_scale + (rb < mb ? rb : mb);
+
+  typedef int codes_t __attribute__((ext_vector_type(FW)));
+  codes_t fa[2][GI], fb[2][GJ];           // codes of two phases
+  const int rowA = (wm * C::RM + r32 * GI) * 128, rowB = (wn * C::RN + r32 * GJ) * 128, sw = r32 & 7;
+  auto fetch = [&](auto ph, const uint8_t* dA, const uint8_t* dB) {
+    constexpr int f = decltype(ph)::value;
+    // a wave's first row is a multiple of 32 GI, so row / GI % 8 is r32 % 8 for all its block rows
+    auto at = [&](const uint8_t* row) {
+      if constexpr (FW == 4) {
+        return *reinterpret_cast<const intx4*>(row + (((2 * f + half) ^ sw) << 4));
+      } else {
+        const intx4 lo = *reinterpret_cast<const intx4*>(row + (((4 * f + 2 * half) ^ sw) << 4));
+        const intx4 hi = *reinterpret_cast<const intx4*>(row + (((4 * f + 2 * half + 1) ^ sw) << 4));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < GJ; ++j) fb[f & 1][j] = at(dB + rowB + j * 128);
+#pragma unroll
+    for (int i = 0; i < GI; ++i) fa[f & 1][i] = at(dA + rowA + i * 128);
+  };
+
+  floatx16 acc[GI][GJ];
+#pragma unroll
+  for (int i = 0; i < GI; ++i)
+#pragma unroll
+    for (int j = 0; j < GJ; ++j) acc[i][j] = floatx16{};
+
+  auto multiply = [&](auto ph, int sa, int sb) {
+    constexpr int u = decltype(ph)::value & 1;
     if constexpr (F32) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen<FB>(fb, s, sb), widen<FA>(fa, s, sa), acc, 0, 0, 0);
+      for (int s = 0; s < 2; ++s) {
+        bf16x8 wa[GI], wb[GJ];
+#pragma unroll
+        for (int j = 0; j < GJ; ++j) wb[j] = widen<FB>(fb[u][j], s, (sb >> (8 * j)) & 255);
+#pragma unroll
+        for (int i = 0; i < GI; ++i) wa[i] = widen<FA>(fa[u][i], s, (sa >> (8 * i)) & 255);
+#pragma unroll
+        for (int i = 0; i < GI; ++i)
+#pragma unroll
+          for (int j = 0; j < GJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
+      }
     } else {
-      acc = mfma8<FB, FA>(fb, fa, acc, sb, sa);
+      auto step = [&](auto ic, auto jc) {
+        constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[u][j], fa[u][i], acc[i][j], FB, FA, j, sb, i, sa);
+      };
+      for_each<GI>([&](auto ic) { for_each<GJ>([&](auto jc) { step(ic, jc); }); });
+    }
+  };
+  auto barrier = [&]() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  // A phase's products run while the next phase's codes come out of LDS.
+  // Before the last phase of a stage every wave has taken that stage's last
+  // codes, so the barrier there frees its buffer for the stage after next,
+  // and the wait before it has this wave's part of the next stage in LDS.
+  int sa[2], sb[2];
+  auto scales = [&](int st, int& va, int& vb) {
+    va = *reinterpret_cast<const WA*>(pa + st * a.a.ld_scale);
+    vb = *reinterpret_cast<const WB*>(pb + st * a.b.ld_scale);
+  };
+  auto stage = [&](int st, auto bc) {
+    constexpr int b = decltype(bc)::value;
+    uint8_t *hereA = b ? sA1 : sA0, *hereB = b ? sB1 : sB0, *nextA = b ? sA0 : sA1, *nextB = b ? sB0 : sB1;
+    const bool more = st + 1 < nst;
+    scales(more ? st + 1 : st, sa[b ^ 1], sb[b ^ 1]);
+    for_each<P>([&](auto ph) {
+      constexpr int f = decltype(ph)::value;
+      if constexpr (f < P - 1) {
+        fetch(std::integral_constant<int, f + 1>{}, hereA, hereB);
+      } else {
+        asm volatile("" ::: "memory");
+        WAIT_LDS();
+        WAIT_VM(2);      // all but this stage's two scale loads, the newest
+        barrier();
+        // past the end the last stage again, into a buffer that nothing reads: no branch between the products
+        copy(st + 2 < nst ? st + 2 : nst - 1, hereA, hereB);
+        asm volatile("" ::: "memory");     // the next stage's scale loads stay behind these
+        fetch(std::integral_constant<int, 0>{}, nextA, nextB);
+      }
+      multiply(ph, sa[b], sb[b]);
+    });
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  if (nst > 0) {
+    scales(0, sa[0], sb[0]);
+    copy(0, sA0, sB0);
+    if (nst > 1) copy(1, sA1, sB1);
+    if (nst > 1) WAIT_VM(C::LA + C::LB);
+    else WAIT_VM(0);
+    barrier();
+    fetch(I0{}, sA0, sB0);
+    for (int st = 0; st < nst; st += 2) {
+      stage(st, I0{});
+      if (st + 1 < nst) stage(st + 1, I1{});
+    }
+    WAIT_VM(0);          // the last copies land before the workgroup gives up its LDS
+  }
+
+  // lane l: row l % 32 of each block row, columns 8 q + 4 (l / 32) + 0..3 of
+  // each block column, which lie GJ apart: 4 GJ neighbours of a row
+  const bool vec = (reinterpret_cast<uintptr_t>(a.c) & 15) == 0 && (a.ldc * (a.c_dtype == OKLS_F32 ? 4 : 2)) % 16 == 0;
+  MatmulArgs o = a;
+  bool part_vec = vec;
+  if (plan.splits > 1) {     // partial sums: (split, m, n up to a multiple of 8) in fp32
+    const int64_t np = (n + 7) & ~int64_t(7);
+    o.c = a.ws + split * m * np;
+    o.ldc = np;
+    o.c_dtype = OKLS_F32;
+    o.accumulate = 0;
+    part_vec = true;
+  }
+#pragma unroll
+  for (int i = 0; i < GI; ++i) {
+    if (ra + i >= m) continue;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t col = n0 + wn * C::RN + (8 * q + 4 * half) * GJ;
+      if (col >= n) continue;
+      float v[4 * GJ];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < GJ; ++j) v[e * GJ + j] = acc[i][j][4 * q + e];
+      store_row<4 * GJ>(o, ra + i, col, v, part_vec);
     }
   }
-  const int64_t row = tm * 16 + (lane & 15), col = tn * 16 + (lane >> 4) * 4;
-  if (row >= m) return;
+}
+
+// c = the partial sums of each element, added in the splits' order
+__global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs a, int splits) {
+  const int64_t m = a.a.rows, n = a.b.rows, np = (n + 7) & ~int64_t(7);
+  const bool vec = (reinterpret_cast<uintptr_t>(a.c) & 15) == 0 && (a.ldc * (a.c_dtype == OKLS_F32 ? 4 : 2)) % 16 == 0;
+  for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 8; i < m * np; i += gridDim.x * 2048ll) {
+    float v[8], u[8];
+    load8(v, a.ws + i, 8, true);
+    for (int s = 1; s < splits; ++s) {
+      load8(u, a.ws + s * m * np + i, 8, true);
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (col + e < n) {
-      const int64_t i = row * a.ldc + col + e;
-      store_any(a.c, i, a.c_dtype, a.accumulate ? acc[e] + load_any(a.c, i, a.c_dtype) : acc[e]);
+      for (int e = 0; e < 8; ++e) v[e] += u[e];
     }
+    const int64_t row = i / np;
+    store_row<8>(a, row, i - row * np, v, vec);
+  }
+}
+
+// Few rows of a (at most 16 TM): c's columns in groups of 16 TN a workgroup,
+// whose waves split the summed axis in turn and add up through LDS.  Every code
+// of b is read once and straight into registers, eight blocks of 128 ahead.
+constexpr int kFewWaves = 8;
+template <int TM, int TN, int FA, int FB, bool F32>
+__global__ __launch_bounds__(kFewWaves * 64) void matmul_few_kernel(MatmulArgs a) {
+  constexpr int U = TM * 1 + TN <= 3 ? 4 : 2;    // blocks of k in flight
+  __shared__ floatx4 part[kFewWaves][TM * TN][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t m = a.a.rows, n = a.b.rows, blocks = (a.a.cols + 127) >> 7;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * TN);
+  int64_t ra[TM], rb[TN];
+  const uint8_t *pa[TM], *pb[TN];
+  // rows past the end read the last one; what they give is not stored
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    ra[i] = 16 * i + (lane & 15) < m ? 16 * i + (lane & 15) : m - 1;
+    pa[i] = a.a.codes + ra[i] * a.a.ld + (lane >> 4) * 32;
+  }
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int64_t r = n0 + 16 * j + (lane & 15);
+    rb[j] = r < n ? r : n - 1;
+    pb[j] = a.b.codes + rb[j] * a.b.ld + (lane >> 4) * 32;
+  }
+  floatx4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = floatx4{};
+  auto run = [&](int64_t k, auto uc) {
+    constexpr int nu = decltype(uc)::value;
+    intx8 fa[nu][TM], fb[nu][TN];
+    int sa[nu][TM], sb[nu][TN];
+#pragma unroll
+    for (int u = 0; u < nu; ++u) {
+      const int64_t kb = k + u * kFewWaves;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        fb[u][j] = frag(pb[j] + kb * 128);
+        sb[u][j] = a.b.scales[kb * a.b.ld_scale + rb[j]];
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        fa[u][i] = frag(pa[i] + kb * 128);
+        sa[u][i] = a.a.scales[kb * a.a.ld_scale + ra[i]];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < nu; ++u) {
+      if constexpr (F32) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          bf16x8 wb[TN];
+#pragma unroll
+          for (int j = 0; j < TN; ++j) wb[j] = widen<FB>(fb[u][j], s, sb[u][j]);
+#pragma unroll
+          for (int i = 0; i < TM; ++i) {
+            const bf16x8 wa = widen<FA>(fa[u][i], s, sa[u][i]);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], wa, acc[i][j], 0, 0, 0);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[u][j], fa[u][i], acc[i][j], FB, FA, 0, sb[u][j], 0, sa[u][i]);
+      }
+    }
+  };
+  int64_t k = wave;
+  for (; k + (U - 1) * kFewWaves < blocks; k += U * kFewWaves) run(k, std::integral_constant<int, U>{});
+  for (; k < blocks; k += kFewWaves) run(k, std::integral_constant<int, 1>{});
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) part[wave][i * TN + j][lane] = acc[i][j];
+  __syncthreads();
+  // lane l of a block holds c[l % 16][4 (l / 16) + e]
+  for (int t = threadIdx.x; t < TM * TN * 64; t += kFewWaves * 64) {
+    const int blk = t >> 6, l = t & 63;
+    floatx4 s = part[0][blk][l];
+#pragma unroll
+    for (int q = 1; q < kFewWaves; ++q) s += part[q][blk][l];
+    const int64_t row = blk / TN * 16 + (l & 15), col = n0 + blk % TN * 16 + (l >> 4) * 4;
+    if (row >= m) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < n) {
+        const int64_t at = row * a.ldc + col + e;
+        store_any(a.c, at, a.c_dtype, a.accumulate ? s[e] + load_any(a.c, at, a.c_dtype) : s[e]);
+      }
+  }
 }
 
 __global__ __launch_bounds__(256) void zero_kernel(void* c, int dtype, int64_t m, int64_t n, int64_t ldc) {
@@ -552,18 +888,54 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-size_t matmul_workspace(int64_t, int64_t, int64_t) { return 0; }
+// Which tile, and into how many parts the summed axis is cut.
+static MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k) {
+  const int64_t blocks = (k + 127) / 128;
+  MatmulPlan p{};
+  p.tm = (m + 255) / 256, p.tn = (n + 255) / 256, p.big = 1, p.splits = 1;
+  if (p.tm * p.tn >= 128) return p;
+  p.big = 0, p.tm = (m + 127) / 128, p.tn = (n + 127) / 128;
+  const int64_t tiles = p.tm * p.tn;
+  int64_t s = 512 / tiles;
+  if (s > blocks / 4) s = blocks / 4;
+  if (s > 16) s = 16;
+  p.splits = s < 2 ? 1 : static_cast<int>(s);
+  return p;
+}
+static bool few_rows(int64_t m) { return m <= 64; }
+
+size_t matmul_workspace(int64_t m, int64_t n, int64_t k) {
+  if (m == 0 || n == 0 || k == 0 || few_rows(m)) return 0;
+  const MatmulPlan p = matmul_plan(m, n, k);
+  return p.splits == 1 ? 0 : static_cast<size_t>(p.splits) * m * ((n + 7) / 8 * 8) * 4;
+}
 
 hipError_t launch_matmul(const MatmulArgs& a, hipStream_t s) {
-  const int64_t m = a.a.rows, n = a.b.rows;
-  if (a.a.cols == 0) {
+  const int64_t m = a.a.rows, n = a.b.rows, k = a.a.cols;
+  if (k == 0) {
     if (!a.accumulate) zero_kernel<<<blocks_up_to((m * n + 255) / 256, 4096), 256, 0, s>>>(a.c, a.c_dtype, m, n, a.ldc);
     return hipGetLastError();
   }
-  const unsigned grid = static_cast<unsigned>((((m + 15) / 16) * ((n + 15) / 16) + 3) / 4);
+  if (few_rows(m)) {
+    by_format(a, [&](auto fa, auto fb, auto f32) {
+      constexpr int FA = decltype(fa)::value, FB = decltype(fb)::value;
+      constexpr bool F32 = decltype(f32)::value;
+      const unsigned one = static_cast<unsigned>((n + 15) / 16), two = static_cast<unsigned>((n + 31) / 32);
+      if (m <= 16) matmul_few_kernel<1, 1, FA, FB, F32><<<one, kFewWaves * 64, 0, s>>>(a);
+      else if (m <= 32) matmul_few_kernel<2, 1, FA, FB, F32><<<one, kFewWaves * 64, 0, s>>>(a);
+      else matmul_few_kernel<4, 2, FA, FB, F32><<<two, kFewWaves * 64, 0, s>>>(a);
+    });
+    return hipGetLastError();
+  }
+  const MatmulPlan p = matmul_plan(m, n, k);
+  const unsigned grid = static_cast<unsigned>(p.tm * p.tn * p.splits);
   by_format(a, [&](auto fa, auto fb, auto f32) {
-    matmul_direct_kernel<decltype(fa)::value, decltype(fb)::value, decltype(f32)::value><<<grid, 256, 0, s>>>(a);
+    constexpr int FA = decltype(fa)::value, FB = decltype(fb)::value;
+    constexpr bool F32 = decltype(f32)::value;
+    if (p.big) matmul_tile_kernel<TileBig, FA, FB, F32><<<grid, TileBig::NT, 0, s>>>(a, p);
+    else matmul_tile_kernel<TileSmall, FA, FB, F32><<<grid, TileSmall::NT, 0, s>>>(a, p);
   });
+  if (p.splits > 1) matmul_join_kernel<<<blocks_up_to((m * ((n + 7) / 8) + 255) / 256, 2048), 256, 0, s>>>(a, p.splits);
   return hipGetLastError();
 }
 
