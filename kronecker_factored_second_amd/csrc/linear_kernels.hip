@@ -491,7 +491,7 @@ using TileSmall = Tile<2, 2, 2, 2>;   // 128 x 128, 4 waves, two workgroups a CU
 struct MatmulPlan {
   int big;         // which tile
   int splits;      // of the summed axis
-  int64_t tm, tn;  // tiles
+  int tm, tn;      // tiles
 };
 
 template <int N> struct ScaleWord { using type = uint32_t; };
@@ -503,6 +503,8 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
   constexpr int P = F32 ? 4 : 2;          // phases of a stage of 128 of k
   constexpr int FW = 16 / P;              // dwords of a lane's codes in a block row and phase
   __shared__ __attribute__((aligned(16))) uint8_t sA0[C::BM * 128], sA1[C::BM * 128], sB0[C::BN * 128], sB1[C::BN * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t e0[512], e1[512];   // scale bytes of the tile's rows, a's and from 256 on b's
+  static_assert(C::BM <= 256 && C::BN <= 256, "one copy holds a side's scales");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int64_t m = a.a.rows, n = a.b.rows;
@@ -510,61 +512,69 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
   // workgroup w runs on XCD w % 8; each XCD takes a run of neighbouring tiles
   // (all splits of it) in bands of 8 tile rows, so that the 32 it holds at a
   // time share operand rows in its L2
-  const int64_t per = plan.tm * plan.tn;
-  const int64_t total = per * plan.splits, w = blockIdx.x, x = w & 7;
-  const int64_t id = x * (total >> 3) + (x < (total & 7) ? x : (total & 7)) + (w >> 3);
-  const int64_t split = id / per, t = id - split * per;
-  const int64_t band = t / (8 * plan.tn), in = t - band * 8 * plan.tn;
-  const int64_t high = plan.tm - band * 8 < 8 ? plan.tm - band * 8 : 8;
-  const int64_t m0 = (band * 8 + in % high) * C::BM, n0 = in / high * C::BN;
+  auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  const unsigned per = plan.tm * plan.tn, total = per * plan.splits, w = blockIdx.x, x = w & 7;
+  const unsigned id = x * (total >> 3) + (x < (total & 7) ? x : (total & 7)) + (w >> 3);
+  const unsigned split = uniform(id / per), t = id - split * per;
+  const unsigned band = uniform(t / (8u * plan.tn)), in = t - band * 8u * plan.tn;
+  const unsigned high = plan.tm - band * 8 < 8 ? plan.tm - band * 8 : 8, column = uniform(in / high);
+  const int64_t m0 = static_cast<int64_t>(band * 8 + in - column * high) * C::BM, n0 = static_cast<int64_t>(column) * C::BN;
 
-  const int64_t blocks = (a.a.cols + 127) >> 7;
-  const int64_t k0 = blocks * split / plan.splits;
-  const int nst = static_cast<int>(blocks * (split + 1) / plan.splits - k0);
+  const unsigned blocks = static_cast<unsigned>((a.a.cols + 127) >> 7);
+  const int k0 = uniform(blocks * split / plan.splits), nst = uniform(blocks * (split + 1) / plan.splits) - k0;
 
-  // copies: 8 rows of 128 bytes each; 16-byte chunk c of row r lies at
-  // position c ^ (r / GI % 8), so that the 16-byte reads of consecutive lanes
-  // (rows GI apart) go to different banks.  Rows past the end read the last
-  // one; what they give is not stored.
-  const uint8_t *ga[C::LA], *gb[C::LB];
+  // Copies: 8 rows of 128 bytes each.  LDS row 32 i + r of a wave's region
+  // holds its row r GI + i, and 16-byte chunk c of it lies at position
+  // c ^ (r / 2 % 8): 16 lanes that read one chunk of 16 consecutive r cover
+  // all 64 banks.  Rows past the end read the last one; what they give is not
+  // stored.
+  // A side's tile spans less than 2^32 bytes (the launcher's rule), so a lane
+  // keeps 32-bit offsets from a base that the whole wave shares.
+  const uint8_t *baseA = a.a.codes + m0 * a.a.ld + k0 * int64_t(128), *baseB = a.b.codes + n0 * a.b.ld + k0 * int64_t(128);
+  uint32_t ga[C::LA], gb[C::LB];
 #pragma unroll
   for (int q = 0; q < C::LA; ++q) {
-    const int row = 8 * (wave + C::NW * q) + (lane >> 3);
-    const int64_t r = m0 + row < m ? m0 + row : m - 1;
-    ga[q] = a.a.codes + r * a.a.ld + k0 * 128 + (((lane & 7) ^ (row / GI & 7)) << 4);
+    const int at = 8 * (wave + C::NW * q) + (lane >> 3), row = at / C::RM * C::RM + (at & 31) * GI + at % C::RM / 32;
+    const int64_t r = m0 + row < m ? row : m - 1 - m0;
+    ga[q] = static_cast<uint32_t>(r * a.a.ld) + (((lane & 7) ^ (at >> 1 & 7)) << 4);
   }
 #pragma unroll
   for (int q = 0; q < C::LB; ++q) {
-    const int row = 8 * (wave + C::NW * q) + (lane >> 3);
-    const int64_t r = n0 + row < n ? n0 + row : n - 1;
-    gb[q] = a.b.codes + r * a.b.ld + k0 * 128 + (((lane & 7) ^ (row / GJ & 7)) << 4);
+    const int at = 8 * (wave + C::NW * q) + (lane >> 3), row = at / C::RN * C::RN + (at & 31) * GJ + at % C::RN / 32;
+    const int64_t r = n0 + row < n ? row : n - 1 - n0;
+    gb[q] = static_cast<uint32_t>(r * a.b.ld) + (((lane & 7) ^ (at >> 1 & 7)) << 4);
   }
-  auto copy = [&](int st, uint8_t* dA, uint8_t* dB) {
+  // scale bytes: one dword a lane, wave 0 those of a and wave 1 those of b
+  // (rows padded to 16 exist; entries past them are another row's)
+  const bool of_b = wave & 1;
+  const int64_t ld_scale = of_b ? a.b.ld_scale : a.a.ld_scale, last = (((of_b ? n : m) + 15) & ~int64_t(15)) - 4 - (of_b ? n0 : m0);
+  const uint8_t* baseS = (of_b ? a.b.scales + n0 : a.a.scales + m0) + k0 * ld_scale;
+  const uint32_t gs = static_cast<uint32_t>(4 * lane < last ? 4 * lane : last);
+  auto copy = [&](int st, uint8_t* dA, uint8_t* dB, uint8_t* e) {
     const int64_t at = static_cast<int64_t>(st) * 128;
 #pragma unroll
     for (int q = 0; q < C::LA; ++q)
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(ga[q] + at),
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(baseA + at + ga[q]),
                                        (__attribute__((address_space(3))) void*)(dA + (wave + C::NW * q) * 1024), 16, 0, 0);
 #pragma unroll
     for (int q = 0; q < C::LB; ++q)
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(gb[q] + at),
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(baseB + at + gb[q]),
                                        (__attribute__((address_space(3))) void*)(dB + (wave + C::NW * q) * 1024), 16, 0, 0);
+    // every wave issues it, in pairs to the same place with the same bytes: no branch between the products
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(baseS + st * ld_scale + gs),
+                                     (__attribute__((address_space(3))) void*)(e + (of_b ? 256 : 0)), 4, 0, 0);
   };
-  // scale bytes of this lane's block rows; rows padded to 16 exist
   const int r32 = lane & 31, half = lane >> 5;
   using WA = typename ScaleWord<GI>::type;
   using WB = typename ScaleWord<GJ>::type;
-  const int64_t ra = m0 + wm * C::RM + r32 * GI, rb = n0 + wn * C::RN + r32 * GJ;
-  const int64_t ma = ((m + 15) & ~int64_t(15)) - GI, mb = ((n + 15) & ~int64_t(15)) - GJ;
-  const uint8_t* pa = a.a.scales + k0 * a.a.ld_scale + (ra < ma ? ra : ma);
-  const uint8_t* pb = a.b.scales + k0 * a.b.ld_scale + (rb < mb ? rb : mb);
+  const int64_t ra = m0 + wm * C::RM + r32 * GI;
 
   typedef int codes_t __attribute__((ext_vector_type(FW)));
   codes_t fa[2][GI], fb[2][GJ];           // codes of two phases
-  const int rowA = (wm * C::RM + r32 * GI) * 128, rowB = (wn * C::RN + r32 * GJ) * 128, sw = r32 & 7;
-  auto fetch = [&](auto ph, const uint8_t* dA, const uint8_t* dB) {
+  const int rowA = (wm * C::RM + r32) * 128, rowB = (wn * C::RN + r32) * 128, sw = r32 >> 1 & 7;
+  int sa, sb, sa_next, sb_next;           // scale bytes of this lane's block rows
+  auto fetch = [&](auto ph, const uint8_t* dA, const uint8_t* dB, const uint8_t* e) {
     constexpr int f = decltype(ph)::value;
-    // a wave's first row is a multiple of 32 GI, so row / GI % 8 is r32 % 8 for all its block rows
     auto at = [&](const uint8_t* row) {
       if constexpr (FW == 4) {
         return *reinterpret_cast<const intx4*>(row + (((2 * f + half) ^ sw) << 4));
@@ -575,9 +585,13 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
       }
     };
 #pragma unroll
-    for (int j = 0; j < GJ; ++j) fb[f & 1][j] = at(dB + rowB + j * 128);
+    for (int j = 0; j < GJ; ++j) fb[f & 1][j] = at(dB + rowB + j * 4096);
 #pragma unroll
-    for (int i = 0; i < GI; ++i) fa[f & 1][i] = at(dA + rowA + i * 128);
+    for (int i = 0; i < GI; ++i) fa[f & 1][i] = at(dA + rowA + i * 4096);
+    if constexpr (f == 0) {
+      sa_next = *reinterpret_cast<const WA*>(e + wm * C::RM + r32 * GI);
+      sb_next = *reinterpret_cast<const WB*>(e + 256 + wn * C::RN + r32 * GJ);
+    }
   };
 
   floatx16 acc[GI][GJ];
@@ -586,7 +600,7 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
 #pragma unroll
     for (int j = 0; j < GJ; ++j) acc[i][j] = floatx16{};
 
-  auto multiply = [&](auto ph, int sa, int sb) {
+  auto multiply = [&](auto ph) {
     constexpr int u = decltype(ph)::value & 1;
     if constexpr (F32) {
 #pragma unroll
@@ -619,43 +633,45 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
   // Before the last phase of a stage every wave has taken that stage's last
   // codes, so the barrier there frees its buffer for the stage after next,
   // and the wait before it has this wave's part of the next stage in LDS.
-  int sa[2], sb[2];
-  auto scales = [&](int st, int& va, int& vb) {
-    va = *reinterpret_cast<const WA*>(pa + st * a.a.ld_scale);
-    vb = *reinterpret_cast<const WB*>(pb + st * a.b.ld_scale);
-  };
   auto stage = [&](int st, auto bc) {
     constexpr int b = decltype(bc)::value;
     uint8_t *hereA = b ? sA1 : sA0, *hereB = b ? sB1 : sB0, *nextA = b ? sA0 : sA1, *nextB = b ? sB0 : sB1;
-    const bool more = st + 1 < nst;
-    scales(more ? st + 1 : st, sa[b ^ 1], sb[b ^ 1]);
+    uint8_t *here = b ? e1 : e0, *next = b ? e0 : e1;
+    sa = sa_next, sb = sb_next;
     for_each<P>([&](auto ph) {
       constexpr int f = decltype(ph)::value;
       if constexpr (f < P - 1) {
-        fetch(std::integral_constant<int, f + 1>{}, hereA, hereB);
+        fetch(std::integral_constant<int, f + 1>{}, hereA, hereB, here);
       } else {
         asm volatile("" ::: "memory");
         WAIT_LDS();
-        WAIT_VM(2);      // all but this stage's two scale loads, the newest
+        WAIT_VM(0);
         barrier();
         // past the end the last stage again, into a buffer that nothing reads: no branch between the products
-        copy(st + 2 < nst ? st + 2 : nst - 1, hereA, hereB);
-        asm volatile("" ::: "memory");     // the next stage's scale loads stay behind these
-        fetch(std::integral_constant<int, 0>{}, nextA, nextB);
+        copy(st + 2 < nst ? st + 2 : nst - 1, hereA, hereB, here);
+        fetch(std::integral_constant<int, 0>{}, nextA, nextB, next);
       }
-      multiply(ph, sa[b], sb[b]);
+      multiply(ph);
+      if constexpr (!F32) {
+        // one product, then its share of the reads and copies
+#pragma unroll
+        for (int q = 0; q < GI * GJ; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, (2 * (GI + GJ) + 2 + GI * GJ - 1) / (GI * GJ), 0);
+          if constexpr (f == P - 1) __builtin_amdgcn_sched_group_barrier(0x020, (C::LA + C::LB + 1 + GI * GJ - 1) / (GI * GJ), 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     });
   };
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
   if (nst > 0) {
-    scales(0, sa[0], sb[0]);
-    copy(0, sA0, sB0);
-    if (nst > 1) copy(1, sA1, sB1);
-    if (nst > 1) WAIT_VM(C::LA + C::LB);
-    else WAIT_VM(0);
+    copy(0, sA0, sB0, e0);
+    copy(nst > 1 ? 1 : 0, sA1, sB1, e1);
+    WAIT_VM(0);
     barrier();
-    fetch(I0{}, sA0, sB0);
+    fetch(I0{}, sA0, sB0, e0);
     for (int st = 0; st < nst; st += 2) {
       stage(st, I0{});
       if (st + 1 < nst) stage(st + 1, I1{});
@@ -710,7 +726,7 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs a, int spli
   }
 }
 
-// Few rows of a (at most 16 TM): c's columns in groups of 16 TN a workgroup,
+// Few rows of a (16 TM of them a workgroup): c's columns in groups of 16 TN a workgroup,
 // whose waves split the summed axis in turn and add up through LDS.  Every code
 // of b is read once and straight into registers, eight blocks of 128 ahead.
 constexpr int kFewWaves = 8;
@@ -720,13 +736,14 @@ __global__ __launch_bounds__(kFewWaves * 64) void matmul_few_kernel(MatmulArgs a
   __shared__ floatx4 part[kFewWaves][TM * TN][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t m = a.a.rows, n = a.b.rows, blocks = (a.a.cols + 127) >> 7;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * TN);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * TN), m0 = static_cast<int64_t>(blockIdx.y) * (16 * TM);
   int64_t ra[TM], rb[TN];
   const uint8_t *pa[TM], *pb[TN];
   // rows past the end read the last one; what they give is not stored
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    ra[i] = 16 * i + (lane & 15) < m ? 16 * i + (lane & 15) : m - 1;
+    const int64_t r = m0 + 16 * i + (lane & 15);
+    ra[i] = r < m ? r : m - 1;
     pa[i] = a.a.codes + ra[i] * a.a.ld + (lane >> 4) * 32;
   }
 #pragma unroll
@@ -796,7 +813,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void matmul_few_kernel(MatmulArgs a
     floatx4 s = part[0][blk][l];
 #pragma unroll
     for (int q = 1; q < kFewWaves; ++q) s += part[q][blk][l];
-    const int64_t row = blk / TN * 16 + (l & 15), col = n0 + blk % TN * 16 + (l >> 4) * 4;
+    const int64_t row = m0 + blk / TN * 16 + (l & 15), col = n0 + blk % TN * 16 + (l >> 4) * 4;
     if (row >= m) continue;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -892,22 +909,21 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s) {
 static MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k) {
   const int64_t blocks = (k + 127) / 128;
   MatmulPlan p{};
-  p.tm = (m + 255) / 256, p.tn = (n + 255) / 256, p.big = 1, p.splits = 1;
-  if (p.tm * p.tn >= 128) return p;
-  p.big = 0, p.tm = (m + 127) / 128, p.tn = (n + 127) / 128;
-  const int64_t tiles = p.tm * p.tn;
+  if (m <= 64) return p;      // no tiles: the few-rows kernel
+  p.tm = static_cast<int>((m + 255) / 256), p.tn = static_cast<int>((n + 255) / 256), p.big = 1, p.splits = 1;
+  if (int64_t(p.tm) * p.tn >= 128) return p;
+  p.big = 0, p.tm = static_cast<int>((m + 127) / 128), p.tn = static_cast<int>((n + 127) / 128);
+  const int64_t tiles = int64_t(p.tm) * p.tn;
   int64_t s = 512 / tiles;
   if (s > blocks / 4) s = blocks / 4;
   if (s > 16) s = 16;
   p.splits = s < 2 ? 1 : static_cast<int>(s);
   return p;
 }
-static bool few_rows(int64_t m) { return m <= 64; }
-
 size_t matmul_workspace(int64_t m, int64_t n, int64_t k) {
-  if (m == 0 || n == 0 || k == 0 || few_rows(m)) return 0;
+  if (m == 0 || n == 0 || k == 0) return 0;
   const MatmulPlan p = matmul_plan(m, n, k);
-  return p.splits == 1 ? 0 : static_cast<size_t>(p.splits) * m * ((n + 7) / 8 * 8) * 4;
+  return p.splits <= 1 ? 0 : static_cast<size_t>(p.splits) * m * ((n + 7) / 8 * 8) * 4;
 }
 
 hipError_t launch_matmul(const MatmulArgs& a, hipStream_t s) {
@@ -916,18 +932,19 @@ hipError_t launch_matmul(const MatmulArgs& a, hipStream_t s) {
     if (!a.accumulate) zero_kernel<<<blocks_up_to((m * n + 255) / 256, 4096), 256, 0, s>>>(a.c, a.c_dtype, m, n, a.ldc);
     return hipGetLastError();
   }
-  if (few_rows(m)) {
+  const MatmulPlan p = matmul_plan(m, n, k);
+  // rows of codes 2^24 bytes apart leave no tile's side inside 2^32 bytes
+  if (p.tm == 0 || a.a.ld >= (1 << 24) || a.b.ld >= (1 << 24)) {
     by_format(a, [&](auto fa, auto fb, auto f32) {
       constexpr int FA = decltype(fa)::value, FB = decltype(fb)::value;
       constexpr bool F32 = decltype(f32)::value;
       const unsigned one = static_cast<unsigned>((n + 15) / 16), two = static_cast<unsigned>((n + 31) / 32);
       if (m <= 16) matmul_few_kernel<1, 1, FA, FB, F32><<<one, kFewWaves * 64, 0, s>>>(a);
       else if (m <= 32) matmul_few_kernel<2, 1, FA, FB, F32><<<one, kFewWaves * 64, 0, s>>>(a);
-      else matmul_few_kernel<4, 2, FA, FB, F32><<<two, kFewWaves * 64, 0, s>>>(a);
+      else matmul_few_kernel<4, 2, FA, FB, F32><<<dim3(two, static_cast<unsigned>((m + 63) / 64)), kFewWaves * 64, 0, s>>>(a);
     });
     return hipGetLastError();
   }
-  const MatmulPlan p = matmul_plan(m, n, k);
   const unsigned grid = static_cast<unsigned>(p.tm * p.tn * p.splits);
   by_format(a, [&](auto fa, auto fb, auto f32) {
     constexpr int FA = decltype(fa)::value, FB = decltype(fb)::value;
