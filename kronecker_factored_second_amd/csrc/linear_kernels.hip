@@ -35,15 +35,9 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(bf16_t v) { return __uint_as_float(static_cast<uint32_t>(v.bits) << 16); }
 __device__ __forceinline__ float to_f32(half_t v) { return static_cast<float>(v); }
 
-// round to nearest even; a NaN keeps its sign and becomes quiet
-__device__ __forceinline__ uint16_t bf16_bits(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return static_cast<uint16_t>((u >> 16) | 0x40u);
-  return static_cast<uint16_t>((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
-}
 template <typename T> __device__ __forceinline__ T from_f32(float f);
 template <> __device__ __forceinline__ float from_f32<float>(float f) { return f; }
-template <> __device__ __forceinline__ bf16_t from_f32<bf16_t>(float f) { return bf16_t{bf16_bits(f)}; }
+template <> __device__ __forceinline__ bf16_t from_f32<bf16_t>(float f) { return bf16_t{__builtin_bit_cast(uint16_t, static_cast<__bf16>(f))}; }
 template <> __device__ __forceinline__ half_t from_f32<half_t>(float f) { return static_cast<half_t>(f); }
 
 // one element of a tensor whose type is known at run time (weights, outputs at an edge)
@@ -443,35 +437,30 @@ __device__ __forceinline__ bf16x8 widen(const V& f, int s, int byte) {
   return r;
 }
 
+#define INLINE __attribute__((always_inline))
 // waits for all but the newest v vector-memory operations, other counters untouched
 #define WAIT_VM(v) __builtin_amdgcn_s_waitcnt(((v) & 15) | (7 << 4) | (15 << 8) | (((v) >> 4) << 14))
 #define WAIT_LDS() __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14))
 
-// c[row][col .. col + N) = v (+ c), the first n of them
-template <int N>
-__device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int64_t col, float (&v)[N], bool vec) {
+// c[row][col .. col + 8) = v (+ c), the first n of them
+__device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int64_t col, float (&v)[8], bool vec) {
   const int64_t i = row * a.ldc + col, left = a.b.rows - col;
-  if (vec && left >= N) {
+  if (vec && left >= 8) {
     auto put = [&](auto* c) {
+      if (a.accumulate) {
+        float w[8];
+        load8(w, c, 8, true);
 #pragma unroll
-      for (int q = 0; q < N; q += 8) {
-        float u[8], w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = v[q + e];
-        if (a.accumulate) {
-          load8(w, c + i + q, 8, true);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[e] += w[e];
-        }
-        store8(c + i + q, u, 8, true);
+        for (int e = 0; e < 8; ++e) v[e] += w[e];
       }
+      store8(c, v, 8, true);
     };
-    if (a.c_dtype == OKLS_F32) put(static_cast<float*>(a.c));
-    else if (a.c_dtype == OKLS_BF16) put(static_cast<bf16_t*>(a.c));
-    else put(static_cast<half_t*>(a.c));
+    if (a.c_dtype == OKLS_F32) put(static_cast<float*>(a.c) + i);
+    else if (a.c_dtype == OKLS_BF16) put(static_cast<bf16_t*>(a.c) + i);
+    else put(static_cast<half_t*>(a.c) + i);
   } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e)
+    for (int e = 0; e < 8; ++e)
       if (e < left) store_any(a.c, i + e, a.c_dtype, a.accumulate ? v[e] + load_any(a.c, i + e, a.c_dtype) : v[e]);
   }
 }
@@ -500,18 +489,21 @@ template <> struct ScaleWord<2> { using type = uint16_t; };
 template <class C, int FA, int FB, bool F32>
 __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, MatmulPlan plan) {
   constexpr int GI = C::GI, GJ = C::GJ;
-  constexpr int P = F32 ? 4 : 2;          // phases of a stage of 128 of k
-  constexpr int FW = 16 / P;              // dwords of a lane's codes in a block row and phase
+  constexpr int P = F32 ? 4 : 2;          // parts of a stage of 128 of k
+  constexpr int FW = 16 / P;              // dwords of a lane's codes in a block row and part
+  constexpr int H = GI / 2;               // block rows of a phase: a phase is half of a's block rows in one part
   __shared__ __attribute__((aligned(16))) uint8_t sA0[C::BM * 128], sA1[C::BM * 128], sB0[C::BN * 128], sB1[C::BN * 128];
   __shared__ __attribute__((aligned(16))) uint8_t e0[512], e1[512];   // scale bytes of the tile's rows, a's and from 256 on b's
+  constexpr int kEdge = 20;               // floats of a row of 16: 16-byte aligned, spread over the banks
+  __shared__ __attribute__((aligned(16))) float edge[C::NW * 32 * kEdge];
   static_assert(C::BM <= 256 && C::BN <= 256, "one copy holds a side's scales");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
   const int64_t m = a.a.rows, n = a.b.rows;
 
-  // workgroup w runs on XCD w % 8; each XCD takes a run of neighbouring tiles
-  // (all splits of it) in bands of 8 tile rows, so that the 32 it holds at a
-  // time share operand rows in its L2
+  // Workgroup w runs on XCD w % 8.  Each XCD takes a run of neighbouring tiles
+  // in bands of 8 tile rows, so that the 32 or 64 it holds at a time share
+  // operand rows in its L2.
   auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
   const unsigned per = plan.tm * plan.tn, total = per * plan.splits, w = blockIdx.x, x = w & 7;
   const unsigned id = x * (total >> 3) + (x < (total & 7) ? x : (total & 7)) + (w >> 3);
@@ -519,7 +511,6 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
   const unsigned band = uniform(t / (8u * plan.tn)), in = t - band * 8u * plan.tn;
   const unsigned high = plan.tm - band * 8 < 8 ? plan.tm - band * 8 : 8, column = uniform(in / high);
   const int64_t m0 = static_cast<int64_t>(band * 8 + in - column * high) * C::BM, n0 = static_cast<int64_t>(column) * C::BN;
-
   const unsigned blocks = static_cast<unsigned>((a.a.cols + 127) >> 7);
   const int k0 = uniform(blocks * split / plan.splits), nst = uniform(blocks * (split + 1) / plan.splits) - k0;
 
@@ -530,7 +521,12 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
   // stored.
   // A side's tile spans less than 2^32 bytes (the launcher's rule), so a lane
   // keeps 32-bit offsets from a base that the whole wave shares.
+  // Scale bytes: one dword a lane, even waves those of a and odd ones those of b
+  // (rows padded to 16 exist; entries past them are another row's).
+  const bool of_b = wave & 1;
+  const int64_t ld_scale = of_b ? a.b.ld_scale : a.a.ld_scale;
   const uint8_t *baseA = a.a.codes + m0 * a.a.ld + k0 * int64_t(128), *baseB = a.b.codes + n0 * a.b.ld + k0 * int64_t(128);
+  const uint8_t* baseS = (of_b ? a.b.scales + n0 : a.a.scales + m0) + k0 * ld_scale;
   uint32_t ga[C::LA], gb[C::LB];
 #pragma unroll
   for (int q = 0; q < C::LA; ++q) {
@@ -544,38 +540,43 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
     const int64_t r = n0 + row < n ? row : n - 1 - n0;
     gb[q] = static_cast<uint32_t>(r * a.b.ld) + (((lane & 7) ^ (at >> 1 & 7)) << 4);
   }
-  // scale bytes: one dword a lane, wave 0 those of a and wave 1 those of b
-  // (rows padded to 16 exist; entries past them are another row's)
-  const bool of_b = wave & 1;
-  const int64_t ld_scale = of_b ? a.b.ld_scale : a.a.ld_scale, last = (((of_b ? n : m) + 15) & ~int64_t(15)) - 4 - (of_b ? n0 : m0);
-  const uint8_t* baseS = (of_b ? a.b.scales + n0 : a.a.scales + m0) + k0 * ld_scale;
-  const uint32_t gs = static_cast<uint32_t>(4 * lane < last ? 4 * lane : last);
-  auto copy = [&](int st, uint8_t* dA, uint8_t* dB, uint8_t* e) {
-    const int64_t at = static_cast<int64_t>(st) * 128;
+  const int64_t last = of_b ? ((n + 15) & ~int64_t(15)) - 4 - n0 : ((m + 15) & ~int64_t(15)) - 4 - m0;
+  uint32_t gs = static_cast<uint32_t>(4 * lane < last ? 4 * lane : last);
+  int copied = 0;
+  auto copy = [&](uint8_t* dA, uint8_t* dB, uint8_t* e) INLINE {
+    // opaque here, so that each stays one 32-bit register next to the uniform base
+#pragma unroll
+    for (int q = 0; q < C::LA; ++q) asm("" : "+v"(ga[q]));
+#pragma unroll
+    for (int q = 0; q < C::LB; ++q) asm("" : "+v"(gb[q]));
+    asm("" : "+v"(gs));
 #pragma unroll
     for (int q = 0; q < C::LA; ++q)
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(baseA + at + ga[q]),
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(baseA + ga[q]),
                                        (__attribute__((address_space(3))) void*)(dA + (wave + C::NW * q) * 1024), 16, 0, 0);
 #pragma unroll
     for (int q = 0; q < C::LB; ++q)
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(baseB + at + gb[q]),
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(baseB + gb[q]),
                                        (__attribute__((address_space(3))) void*)(dB + (wave + C::NW * q) * 1024), 16, 0, 0);
-    // every wave issues it, in pairs to the same place with the same bytes: no branch between the products
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(baseS + st * ld_scale + gs),
+    // every wave issues it, several to the same place with the same bytes: no branch between the products
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(baseS + gs),
                                      (__attribute__((address_space(3))) void*)(e + (of_b ? 256 : 0)), 4, 0, 0);
+    // past the end the last stage again, into a buffer that nothing reads: no branch between the products
+    const int64_t on = ++copied < nst ? 1 : 0;
+    baseA += on * 128, baseB += on * 128, baseS += on * ld_scale;
   };
   const int r32 = lane & 31, half = lane >> 5;
   using WA = typename ScaleWord<GI>::type;
   using WB = typename ScaleWord<GJ>::type;
-  const int64_t ra = m0 + wm * C::RM + r32 * GI;
 
   typedef int codes_t __attribute__((ext_vector_type(FW)));
-  codes_t fa[2][GI], fb[2][GJ];           // codes of two phases
+  codes_t fa[2][H], fb[2][GJ];            // codes of two phases, of two parts
   const int rowA = (wm * C::RM + r32) * 128, rowB = (wn * C::RN + r32) * 128, sw = r32 >> 1 & 7;
   int sa, sb, sa_next, sb_next;           // scale bytes of this lane's block rows
-  auto fetch = [&](auto ph, const uint8_t* dA, const uint8_t* dB, const uint8_t* e) {
-    constexpr int f = decltype(ph)::value;
-    auto at = [&](const uint8_t* row) {
+  // the codes of phase u; b's with a part's first
+  auto fetch = [&](auto uc, const uint8_t* dA, const uint8_t* dB, const uint8_t* e) INLINE {
+    constexpr int u = decltype(uc)::value, f = u / 2, g = u & 1;
+    auto at = [&](const uint8_t* row) INLINE {
       if constexpr (FW == 4) {
         return *reinterpret_cast<const intx4*>(row + (((2 * f + half) ^ sw) << 4));
       } else {
@@ -584,46 +585,45 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       }
     };
+    if constexpr (g == 0)
 #pragma unroll
-    for (int j = 0; j < GJ; ++j) fb[f & 1][j] = at(dB + rowB + j * 4096);
+      for (int j = 0; j < GJ; ++j) fb[f & 1][j] = at(dB + rowB + j * 4096);
 #pragma unroll
-    for (int i = 0; i < GI; ++i) fa[f & 1][i] = at(dA + rowA + i * 4096);
-    if constexpr (f == 0) {
+    for (int i = 0; i < H; ++i) fa[g][i] = at(dA + rowA + (g * H + i) * 4096);
+    if constexpr (u == 0) {
       sa_next = *reinterpret_cast<const WA*>(e + wm * C::RM + r32 * GI);
       sb_next = *reinterpret_cast<const WB*>(e + 256 + wn * C::RN + r32 * GJ);
     }
   };
 
   floatx16 acc[GI][GJ];
-#pragma unroll
-  for (int i = 0; i < GI; ++i)
-#pragma unroll
-    for (int j = 0; j < GJ; ++j) acc[i][j] = floatx16{};
 
-  auto multiply = [&](auto ph) {
-    constexpr int u = decltype(ph)::value & 1;
+  auto multiply = [&](auto uc) INLINE {
+    constexpr int f = decltype(uc)::value / 2, g = decltype(uc)::value & 1;
     if constexpr (F32) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        bf16x8 wa[GI], wb[GJ];
+        bf16x8 wa[H], wb[GJ];
 #pragma unroll
-        for (int j = 0; j < GJ; ++j) wb[j] = widen<FB>(fb[u][j], s, (sb >> (8 * j)) & 255);
+        for (int j = 0; j < GJ; ++j) wb[j] = widen<FB>(fb[f & 1][j], s, (sb >> (8 * j)) & 255);
 #pragma unroll
-        for (int i = 0; i < GI; ++i) wa[i] = widen<FA>(fa[u][i], s, (sa >> (8 * i)) & 255);
+        for (int i = 0; i < H; ++i) wa[i] = widen<FA>(fa[g][i], s, (sa >> (8 * (g * H + i))) & 255);
 #pragma unroll
-        for (int i = 0; i < GI; ++i)
+        for (int i = 0; i < H; ++i)
 #pragma unroll
-          for (int j = 0; j < GJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < GJ; ++j)
+            acc[g * H + i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[g * H + i][j], 0, 0, 0);
       }
     } else {
-      auto step = [&](auto ic, auto jc) {
-        constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[u][j], fa[u][i], acc[i][j], FB, FA, j, sb, i, sa);
-      };
-      for_each<GI>([&](auto ic) { for_each<GJ>([&](auto jc) { step(ic, jc); }); });
+      for_each<H>([&](auto ic) INLINE {
+        for_each<GJ>([&](auto jc) INLINE {
+          constexpr int i = decltype(ic)::value, j = decltype(jc)::value, at = g * H + i;
+          acc[at][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[f & 1][j], fa[g][i], acc[at][j], FB, FA, j, sb, at, sa);
+        });
+      });
     }
   };
-  auto barrier = [&]() {
+  auto barrier = [&]() INLINE {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -633,80 +633,129 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
   // Before the last phase of a stage every wave has taken that stage's last
   // codes, so the barrier there frees its buffer for the stage after next,
   // and the wait before it has this wave's part of the next stage in LDS.
-  auto stage = [&](int st, auto bc) {
+  auto stage = [&](auto bc) INLINE {
     constexpr int b = decltype(bc)::value;
     uint8_t *hereA = b ? sA1 : sA0, *hereB = b ? sB1 : sB0, *nextA = b ? sA0 : sA1, *nextB = b ? sB0 : sB1;
-    uint8_t *here = b ? e1 : e0, *next = b ? e0 : e1;
+    uint8_t *hereE = b ? e1 : e0, *nextE = b ? e0 : e1;
     sa = sa_next, sb = sb_next;
-    for_each<P>([&](auto ph) {
-      constexpr int f = decltype(ph)::value;
-      if constexpr (f < P - 1) {
-        fetch(std::integral_constant<int, f + 1>{}, hereA, hereB, here);
+    for_each<2 * P>([&](auto uc) INLINE {
+      constexpr int u = decltype(uc)::value;
+      constexpr bool final = u == 2 * P - 1;
+      if constexpr (!final) {
+        fetch(std::integral_constant<int, u + 1>{}, hereA, hereB, hereE);
       } else {
         asm volatile("" ::: "memory");
         WAIT_LDS();
         WAIT_VM(0);
         barrier();
-        // past the end the last stage again, into a buffer that nothing reads: no branch between the products
-        copy(st + 2 < nst ? st + 2 : nst - 1, hereA, hereB, here);
-        fetch(std::integral_constant<int, 0>{}, nextA, nextB, next);
+        copy(hereA, hereB, hereE);
+        fetch(std::integral_constant<int, 0>{}, nextA, nextB, nextE);
       }
-      multiply(ph);
+      multiply(uc);
       if constexpr (!F32) {
         // one product, then its share of the reads and copies
 #pragma unroll
-        for (int q = 0; q < GI * GJ; ++q) {
+        for (int q = 0; q < H * GJ; ++q) {
+          constexpr int n = H * GJ, reads = 2 * (H + (u & 1 ? GJ : 0) + final), copies = final ? C::LA + C::LB + 1 : 0;
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, (2 * (GI + GJ) + 2 + GI * GJ - 1) / (GI * GJ), 0);
-          if constexpr (f == P - 1) __builtin_amdgcn_sched_group_barrier(0x020, (C::LA + C::LB + 1 + GI * GJ - 1) / (GI * GJ), 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, (reads + n - 1) / n, 0);
+          __builtin_amdgcn_sched_group_barrier(0x020, (copies + n - 1) / n, 0);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     });
   };
-  using I0 = std::integral_constant<int, 0>;
-  using I1 = std::integral_constant<int, 1>;
-  if (nst > 0) {
-    copy(0, sA0, sB0, e0);
-    copy(nst > 1 ? 1 : 0, sA1, sB1, e1);
-    WAIT_VM(0);
-    barrier();
-    fetch(I0{}, sA0, sB0, e0);
-    for (int st = 0; st < nst; st += 2) {
-      stage(st, I0{});
-      if (st + 1 < nst) stage(st + 1, I1{});
-    }
-    WAIT_VM(0);          // the last copies land before the workgroup gives up its LDS
-  }
 
-  // lane l: row l % 32 of each block row, columns 8 q + 4 (l / 32) + 0..3 of
-  // each block column, which lie GJ apart: 4 GJ neighbours of a row
-  const bool vec = (reinterpret_cast<uintptr_t>(a.c) & 15) == 0 && (a.ldc * (a.c_dtype == OKLS_F32 ? 4 : 2)) % 16 == 0;
   MatmulArgs o = a;
-  bool part_vec = vec;
+  const int64_t np = (n + 7) & ~int64_t(7);
   if (plan.splits > 1) {     // partial sums: (split, m, n up to a multiple of 8) in fp32
-    const int64_t np = (n + 7) & ~int64_t(7);
-    o.c = a.ws + split * m * np;
     o.ldc = np;
     o.c_dtype = OKLS_F32;
     o.accumulate = 0;
-    part_vec = true;
   }
+  // lane l: row l % 32 of each block row, columns 8 q + 4 (l / 32) + 0..3 of
+  // each block column, which lie GJ apart: 8 neighbours of a row
+  static_assert(GJ == 2, "a lane's neighbours are one 16-byte store of a 16-bit result");
+  auto finish = [&]() INLINE {
+    if (plan.splits > 1) o.c = a.ws + split * m * np;
+    const int64_t r0 = m0 + wm * C::RM, c0 = n0 + wn * C::RN;
+    const int size = o.c_dtype == OKLS_F32 ? 4 : 2;
+    const bool vec = (reinterpret_cast<uintptr_t>(o.c) & 15) == 0 && (o.ldc * size) % 16 == 0 && c0 + C::RN <= n;
+    auto each = [&](auto f) INLINE {
 #pragma unroll
-  for (int i = 0; i < GI; ++i) {
-    if (ra + i >= m) continue;
+      for (int i = 0; i < GI; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t col = n0 + wn * C::RN + (8 * q + 4 * half) * GJ;
-      if (col >= n) continue;
-      float v[4 * GJ];
+        for (int q = 0; q < 4; ++q) {
+          float v[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int j = 0; j < GJ; ++j) v[e * GJ + j] = acc[i][j][4 * q + e];
-      store_row<4 * GJ>(o, ra + i, col, v, part_vec);
+            for (int j = 0; j < GJ; ++j) v[e * GJ + j] = acc[i][j][4 * q + e];
+          f(i, q, v);
+        }
+    };
+    auto rows = [&](auto* c) INLINE {
+      auto* at = c + (r0 + r32 * GI) * o.ldc + c0 + 8 * half;
+      each([&](int i, int q, float (&v)[8]) INLINE {
+        if (r0 + r32 * GI + i >= m) return;
+        auto* to = at + i * o.ldc + 16 * q;
+        if (o.accumulate) {
+          float u[8];
+          load8(u, to, 8, true);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += u[e];
+        }
+        store8(to, v, 8, true);
+      });
+    };
+    if (vec) {
+      if (F32 || o.c_dtype == OKLS_F32) rows(static_cast<float*>(o.c));
+      else if (o.c_dtype == OKLS_BF16) rows(static_cast<bf16_t*>(o.c));
+      else rows(static_cast<half_t*>(o.c));
+      return;
     }
+    // Rows that end inside the region or do not start on 16 bytes: 32 x 16
+    // elements at a time through LDS, so that 16 lanes write neighbours
+    // (single elements straight from the lanes touch 64 rows a store).
+    float* mine = edge + wave * 32 * kEdge;
+    each([&](int i, int q, float (&v)[8]) INLINE {
+      asm volatile("" ::: "memory");
+      *reinterpret_cast<floatx4*>(mine + r32 * kEdge + 8 * half) = floatx4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<floatx4*>(mine + r32 * kEdge + 8 * half + 4) = floatx4{v[4], v[5], v[6], v[7]};
+      WAIT_LDS();
+      asm volatile("" ::: "memory");
+      const int64_t col = c0 + 16 * q + (lane & 15);
+#pragma unroll 2
+      for (int t = 0; t < 8; ++t) {
+        const int r = 4 * t + (lane >> 4);
+        const int64_t row = r0 + r * GI + i;
+        const float x = mine[r * kEdge + (lane & 15)];
+        if (row < m && col < n) {
+          const int64_t to = row * o.ldc + col;
+          store_any(o.c, to, o.c_dtype, o.accumulate ? x + load_any(o.c, to, o.c_dtype) : x);
+        }
+      }
+      WAIT_LDS();
+    });
+  };
+
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  copy(sA0, sB0, e0);
+  copy(sA1, sB1, e1);
+#pragma unroll
+  for (int i = 0; i < GI; ++i)
+#pragma unroll
+    for (int j = 0; j < GJ; ++j) acc[i][j] = floatx16{};
+  WAIT_VM(C::LA + C::LB + 1);
+  barrier();
+  fetch(I0{}, sA0, sB0, e0);
+  for (int st = 0; st < nst; st += 2) {
+    stage(I0{});
+    if (st + 1 < nst) stage(I1{});
   }
+  WAIT_VM(0);              // the last copies land before the workgroup gives up its LDS
+  finish();
 }
 
 // c = the partial sums of each element, added in the splits' order
@@ -722,7 +771,7 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs a, int spli
       for (int e = 0; e < 8; ++e) v[e] += u[e];
     }
     const int64_t row = i / np;
-    store_row<8>(a, row, i - row * np, v, vec);
+    store_row(a, row, i - row * np, v, vec);
   }
 }
 
@@ -945,12 +994,12 @@ hipError_t launch_matmul(const MatmulArgs& a, hipStream_t s) {
     });
     return hipGetLastError();
   }
-  const unsigned grid = static_cast<unsigned>(p.tm * p.tn * p.splits);
+  const unsigned tiles = static_cast<unsigned>(p.tm * p.tn * p.splits);
   by_format(a, [&](auto fa, auto fb, auto f32) {
     constexpr int FA = decltype(fa)::value, FB = decltype(fb)::value;
     constexpr bool F32 = decltype(f32)::value;
-    if (p.big) matmul_tile_kernel<TileBig, FA, FB, F32><<<grid, TileBig::NT, 0, s>>>(a, p);
-    else matmul_tile_kernel<TileSmall, FA, FB, F32><<<grid, TileSmall::NT, 0, s>>>(a, p);
+    if (p.big) matmul_tile_kernel<TileBig, FA, FB, F32><<<tiles, TileBig::NT, 0, s>>>(a, p);
+    else matmul_tile_kernel<TileSmall, FA, FB, F32><<<tiles, TileSmall::NT, 0, s>>>(a, p);
   });
   if (p.splits > 1) matmul_join_kernel<<<blocks_up_to((m * ((n + 7) / 8) + 255) / 256, 2048), 256, 0, s>>>(a, p.splits);
   return hipGetLastError();
