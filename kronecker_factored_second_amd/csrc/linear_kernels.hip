@@ -53,16 +53,19 @@ __device__ __forceinline__ void store_any(void* p, int64_t i, int dtype, float v
 }
 
 // Eight consecutive elements as fp32; the first n of them (n <= 8) exist, the
-// others are zero.  vec: p is 16-byte aligned.
+// others are zero.  Global memory takes 16-byte accesses at any element's
+// alignment, so rows that start anywhere need no path of their own.
+typedef u16x8 u16x8_any __attribute__((aligned(2)));
+typedef floatx4 floatx4_any __attribute__((aligned(4)));
 template <typename T>
-__device__ __forceinline__ void load8(float (&v)[8], const T* p, int n, bool vec) {
-  if (n >= 8 && vec) {
+__device__ __forceinline__ void load8(float (&v)[8], const T* p, int n) {
+  if (n >= 8) {
     if constexpr (sizeof(T) == 4) {
-      const floatx4 a = reinterpret_cast<const floatx4*>(p)[0], b = reinterpret_cast<const floatx4*>(p)[1];
+      const floatx4 a = reinterpret_cast<const floatx4_any*>(p)[0], b = reinterpret_cast<const floatx4_any*>(p)[1];
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
     } else {
-      const u16x8 a = *reinterpret_cast<const u16x8*>(p);
+      const u16x8 a = *reinterpret_cast<const u16x8_any*>(p);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if constexpr (__is_same(T, bf16_t)) v[j] = to_f32(bf16_t{a[j]});
@@ -75,16 +78,16 @@ __device__ __forceinline__ void load8(float (&v)[8], const T* p, int n, bool vec
   }
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8], int n, bool vec) {
-  if (n >= 8 && vec) {
+__device__ __forceinline__ void store8(T* p, const float (&v)[8], int n) {
+  if (n >= 8) {
     if constexpr (sizeof(T) == 4) {
-      reinterpret_cast<floatx4*>(p)[0] = floatx4{v[0], v[1], v[2], v[3]};
-      reinterpret_cast<floatx4*>(p)[1] = floatx4{v[4], v[5], v[6], v[7]};
+      reinterpret_cast<floatx4_any*>(p)[0] = floatx4{v[0], v[1], v[2], v[3]};
+      reinterpret_cast<floatx4_any*>(p)[1] = floatx4{v[4], v[5], v[6], v[7]};
     } else {
       u16x8 a;
 #pragma unroll
       for (int j = 0; j < 8; ++j) a[j] = __builtin_bit_cast(uint16_t, from_f32<T>(v[j]));
-      *reinterpret_cast<u16x8*>(p) = a;
+      *reinterpret_cast<u16x8_any*>(p) = a;
     }
   } else {
 #pragma unroll
@@ -93,16 +96,9 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n, bool ve
   }
 }
 __device__ __forceinline__ void load8_any(float (&v)[8], const void* p, int64_t i, int n, int dtype) {
-  if (dtype == OKLS_F32) {
-    const float* q = static_cast<const float*>(p) + i;
-    load8(v, q, n, (reinterpret_cast<uintptr_t>(q) & 15) == 0);
-  } else if (dtype == OKLS_BF16) {
-    const bf16_t* q = static_cast<const bf16_t*>(p) + i;
-    load8(v, q, n, (reinterpret_cast<uintptr_t>(q) & 15) == 0);
-  } else {
-    const half_t* q = static_cast<const half_t*>(p) + i;
-    load8(v, q, n, (reinterpret_cast<uintptr_t>(q) & 15) == 0);
-  }
+  if (dtype == OKLS_F32) load8(v, static_cast<const float*>(p) + i, n);
+  else if (dtype == OKLS_BF16) load8(v, static_cast<const bf16_t*>(p) + i, n);
+  else load8(v, static_cast<const half_t*>(p) + i, n);
 }
 
 __device__ __forceinline__ int clamp8(int64_t left) { return left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0; }
@@ -163,7 +159,6 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
   const int t = threadIdx.x, c8 = t & 15, rg = t >> 4, wave = t >> 6;
   const int64_t tiles_c = (a.cols + 127) >> 7, n_tiles = tiles_c * ((a.rows + 127) >> 7);
   const T* x = static_cast<const T*>(a.x);
-  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (a.ldx * sizeof(T)) % 16 == 0;
   for (int64_t it = blockIdx.x; it < n_tiles; it += gridDim.x) {
     const int64_t br = it / tiles_c, bc = it - br * tiles_c;
     const int64_t r0 = br * 128 + rg * 8, c0 = bc * 128 + c8 * 8;
@@ -171,7 +166,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
     float v[8][8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      if (r0 + p < a.rows) load8(v[p], x + (r0 + p) * a.ldx + c0, nc, vec);
+      if (r0 + p < a.rows) load8(v[p], x + (r0 + p) * a.ldx + c0, nc);
       else
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[p][j] = 0.0f;
@@ -253,54 +248,52 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
 // Norm
 // ---------------------------------------------------------------------------
 
-// the sum of v over the block's four waves, in every thread, in a fixed order
-template <typename V>
-__device__ __forceinline__ V block_sum(V v, V* sh) {
+// A row by a wave (THR = 64) or by a workgroup's four (THR = 256), its NC
+// chunks of 8 elements a thread held in registers from the one read of it.
+// Wider rows (NC = 0) are read again for the second pass.
+constexpr int kThreads = 256;
+
+// the sum of v over a row's threads, in each of them, in a fixed order
+template <int THR, typename V>
+__device__ __forceinline__ V row_sum(V v, V* sh) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = sh[0] + sh[1] + sh[2] + sh[3];
-  __syncthreads();
+  if constexpr (THR == 256) {
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = sh[0] + sh[1] + sh[2] + sh[3];
+    __syncthreads();
+  }
   return v;
 }
 
-template <typename T, int FMT>
-__global__ __launch_bounds__(256) void rms_norm_kernel(NormArgs a) {
+template <typename T, int FMT, int THR, int NC>
+__global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
   __shared__ double sh[4];
-  const int t = threadIdx.x;
+  constexpr int ROWS = kThreads / THR;
+  const int t = threadIdx.x % THR;
   const T* x = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.residual);
   T* hs = static_cast<T*>(a.h);
-  auto al = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * sizeof(T)) % 16 == 0; };
-  const bool vx = al(x, a.ldx), vr = al(res, a.ldr), vh = al(hs, a.ldh);
   const int64_t chunks = ((a.cols + 127) >> 7) * 16;   // whole blocks: past the end v = 0
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    auto value = [&](float (&v)[8], int64_t c, bool first) {
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / THR; row < a.rows; row += static_cast<int64_t>(gridDim.x) * ROWS) {
+    auto read = [&](float (&v)[8], int64_t c) { load8(v, x + row * a.ldx + c * 8, clamp8(a.cols - c * 8)); };
+    auto add = [&](float (&v)[8], int64_t c, bool store) {
       const int n = clamp8(a.cols - c * 8);
-      load8(v, x + row * a.ldx + c * 8, n, vx);
-      if (res != nullptr) {
-        float r[8];
-        load8(r, res + row * a.ldr + c * 8, n, vr);
+      float r[8];
+      load8(r, res + row * a.ldr + c * 8, n);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = to_f32(from_f32<T>(v[j] + r[j]));
-        if (first) store8(hs + row * a.ldh + c * 8, v, n, vh);
-      }
-      return n;
+      for (int j = 0; j < 8; ++j) v[j] = to_f32(from_f32<T>(v[j] + r[j]));
+      if (store) store8(hs + row * a.ldh + c * 8, v, n);
     };
-    double ss = 0.0;
-    for (int64_t c = t; c < chunks; c += 256) {
-      float v[8];
-      value(v, c, true);
+    auto squares = [&](const float (&v)[8], double ss) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), ss);
-    }
-    ss = block_sum(ss, sh);
-    const float rstd = static_cast<float>(1.0 / sqrt(ss / static_cast<double>(a.cols) + static_cast<double>(a.eps)));
-    if (t == 0) a.rstd[row] = rstd;
-    for (int64_t c = t; c < chunks; c += 256) {
-      float v[8], w[8];
-      const int n = value(v, c, false);
+      return ss;
+    };
+    auto write = [&](float (&v)[8], int64_t c, float rstd) {
+      const int n = clamp8(a.cols - c * 8);
+      float w[8];
       load8_any(w, a.weight, c * 8, n, a.weight_dtype);
       uint32_t top = 0;
 #pragma unroll
@@ -313,73 +306,176 @@ __global__ __launch_bounds__(256) void rms_norm_kernel(NormArgs a) {
       const uint32_t byte = scale_byte<FMT>(top);
       *reinterpret_cast<uint2*>(a.out.codes + row * a.out.ld + c * 8) = codes8<FMT>(v, scale_inverse(byte));
       if ((t & 15) == 0) a.out.scales[(c >> 4) * a.out.ld_scale + row] = static_cast<uint8_t>(byte);
+    };
+    auto rms = [&](double ss) {
+      ss = row_sum<THR>(ss, sh);
+      const float rstd = static_cast<float>(1.0 / sqrt(ss / static_cast<double>(a.cols) + static_cast<double>(a.eps)));
+      if (t == 0) a.rstd[row] = rstd;
+      return rstd;
+    };
+    double ss = 0.0;
+    if constexpr (NC != 0) {
+      float v[NC][8];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) read(v[i], t + i * THR);      // nothing past the end
+      if (res != nullptr)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) add(v[i], t + i * THR, true);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) ss = squares(v[i], ss);
+      const float rstd = rms(ss);
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (t + i * THR < chunks) write(v[i], t + i * THR, rstd);
+    } else {
+      float v[8];
+      for (int64_t c = t; c < chunks; c += THR) {
+        read(v, c);
+        if (res != nullptr) add(v, c, true);
+        ss = squares(v, ss);
+      }
+      const float rstd = rms(ss);
+      for (int64_t c = t; c < chunks; c += THR) {
+        read(v, c);
+        if (res != nullptr) add(v, c, false);
+        write(v, c, rstd);
+      }
     }
   }
 }
 
 constexpr int kGradBlocks = 512;   // most blocks of a launch, each with one row of partial sums of dweight
 
-template <typename T>
-__global__ __launch_bounds__(256) void norm_grad_kernel(NormGradArgs a) {
+// The same layout.  A thread meets the same columns in every row, so dweight's
+// sums stay in its registers; a workgroup leaves one row of partial sums.
+template <typename T, int THR, int NC>
+__global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs a) {
+  constexpr int ROWS = kThreads / THR;
   __shared__ float sh[4];
-  const int t = threadIdx.x;
+  const int t = threadIdx.x % THR;
   const T* dy = static_cast<const T*>(a.dy);
   const T* h = static_cast<const T*>(a.h);
   const T* dh = static_cast<const T*>(a.dh);
   T* dx = static_cast<T*>(a.dx);
-  auto al = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * sizeof(T)) % 16 == 0; };
-  const bool vy = al(dy, a.lddy), vh = al(h, a.ldh), vd = al(dh, a.lddh), vx = al(dx, a.lddx);
   const int64_t chunks = (a.cols + 7) >> 3;
   float* part = a.ws + blockIdx.x * (chunks * 8);
-  for (int64_t c = t; c < chunks; c += 256)
+  const float inv = 1.0f / static_cast<float>(a.cols);
+  auto dot8 = [&](const float (&g)[8], const float (&u)[8], const float (&w)[8], float rstd, float dot) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[c * 8 + j] = 0.0f;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const float rstd = a.rstd[row];
-    float dot = 0.0f;
-    for (int64_t c = t; c < chunks; c += 256) {
-      const int n = clamp8(a.cols - c * 8);
-      float g[8], u[8], w[8];
-      load8(g, dy + row * a.lddy + c * 8, n, vy);
-      load8(u, h + row * a.ldh + c * 8, n, vh);
-      load8_any(w, a.weight, c * 8, n, a.weight_dtype);
+    for (int j = 0; j < 8; ++j) dot = fmaf(g[j] * w[j], u[j] * rstd, dot);
+    return dot;
+  };
+  auto finish8 = [&](float (&g)[8], float (&u)[8], const float (&w)[8], float (&sum)[8], float rstd, float mean, int64_t row, int64_t c, int n) {
+    float d[8] = {};
+    if (dh != nullptr) load8(d, dh + row * a.lddh + c * 8, n);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) dot = fmaf(g[j] * w[j], u[j] * rstd, dot);
+    for (int j = 0; j < 8; ++j) {
+      const float hat = u[j] * rstd;
+      sum[j] = fmaf(g[j], hat, sum[j]);
+      u[j] = fmaf(rstd, g[j] * w[j] - hat * mean, d[j]);
     }
-    const float mean = block_sum(dot, sh) / static_cast<float>(a.cols);
-    for (int64_t c = t; c < chunks; c += 256) {
-      const int n = clamp8(a.cols - c * 8);
-      float g[8], u[8], w[8], d[8];
-      load8(g, dy + row * a.lddy + c * 8, n, vy);
-      load8(u, h + row * a.ldh + c * 8, n, vh);
-      load8_any(w, a.weight, c * 8, n, a.weight_dtype);
-      if (dh != nullptr) load8(d, dh + row * a.lddh + c * 8, n, vd);
-      else
+    store8(dx + row * a.lddx + c * 8, u, n);
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
+  if constexpr (NC != 0) {
+    float sum[NC][8] = {};
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / THR; row < a.rows; row += step) {
+      const float rstd = a.rstd[row];
+      float g[NC][8], u[NC][8], dot = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float hat = u[j] * rstd;
-        part[c * 8 + j] = fmaf(g[j], hat, part[c * 8 + j]);
-        u[j] = fmaf(rstd, g[j] * w[j] - hat * mean, d[j]);
+      for (int i = 0; i < NC; ++i) {
+        const int64_t c = t + i * THR;
+        const int n = clamp8(a.cols - c * 8);
+        load8(g[i], dy + row * a.lddy + c * 8, n);
+        load8(u[i], h + row * a.ldh + c * 8, n);
       }
-      store8(dx + row * a.lddx + c * 8, u, n, vx);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int64_t c = t + i * THR;
+        float w[8];
+        load8_any(w, a.weight, c * 8, clamp8(a.cols - c * 8), a.weight_dtype);
+        dot = dot8(g[i], u[i], w, rstd, dot);
+      }
+      const float mean = row_sum<THR>(dot, sh) * inv;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int64_t c = t + i * THR;
+        const int n = clamp8(a.cols - c * 8);
+        float w[8];
+        load8_any(w, a.weight, c * 8, n, a.weight_dtype);
+        finish8(g[i], u[i], w, sum[i], rstd, mean, row, c, n);
+      }
+    }
+    if constexpr (ROWS > 1) {
+      // the waves' sums, added in their order
+      __shared__ float joined[ROWS][8][THR];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int me = threadIdx.x / THR;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) joined[me][j][t] = sum[i][j];
+        __syncthreads();
+        for (int e = threadIdx.x; e < 8 * THR; e += kThreads) {
+          const int64_t col = static_cast<int64_t>(i) * THR * 8 + e;
+          float s = 0.0f;
+#pragma unroll
+          for (int q = 0; q < ROWS; ++q) s += joined[q][e & 7][e >> 3];
+          if (col < chunks * 8) part[col] = s;
+        }
+        __syncthreads();
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (t + i * THR < chunks) store8(part + (t + i * THR) * 8, sum[i], 8);
+    }
+  } else {
+    for (int64_t c = t; c < chunks; c += THR)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) part[c * 8 + j] = 0.0f;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+      const float rstd = a.rstd[row];
+      float g[8], u[8], w[8], sum[8], dot = 0.0f;
+      auto read = [&](int64_t c, int n) {
+        load8(g, dy + row * a.lddy + c * 8, n);
+        load8(u, h + row * a.ldh + c * 8, n);
+        load8_any(w, a.weight, c * 8, n, a.weight_dtype);
+      };
+      for (int64_t c = t; c < chunks; c += THR) {
+        read(c, clamp8(a.cols - c * 8));
+        dot = dot8(g, u, w, rstd, dot);
+      }
+      const float mean = row_sum<THR>(dot, sh) * inv;
+      for (int64_t c = t; c < chunks; c += THR) {
+        const int n = clamp8(a.cols - c * 8);
+        read(c, n);
+        load8(sum, part + c * 8, 8);
+        finish8(g, u, w, sum, rstd, mean, row, c, n);
+        store8(part + c * 8, sum, 8);
+      }
     }
   }
 }
 
-// dweight[c] = the partial sums of column c, added in fp64 in the blocks' order
-__global__ __launch_bounds__(256) void norm_dw_kernel(const float* part, int n_parts, int64_t stride, int64_t cols, void* dweight, int dtype) {
-  __shared__ double sh[4][64];
-  const int c = threadIdx.x & 63, g = threadIdx.x >> 6;
-  for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * 64; c0 < cols; c0 += static_cast<int64_t>(gridDim.x) * 64) {
+// dweight[c] = the partial sums of column c, added in fp64: 32 groups of blocks
+// in their order, then the groups in theirs
+__global__ __launch_bounds__(1024) void norm_dw_kernel(const float* part, int n_parts, int64_t stride, int64_t cols, void* dweight, int dtype) {
+  __shared__ double sh[32][33];
+  const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
+  for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * 32; c0 < cols; c0 += static_cast<int64_t>(gridDim.x) * 32) {
     double s = 0.0;
-    if (c0 + c < cols)
-      for (int p = g; p < n_parts; p += 4) s += static_cast<double>(part[p * stride + c0 + c]);
+    if (c0 + c < cols) {
+#pragma unroll 8
+      for (int p = g; p < n_parts; p += 32) s += static_cast<double>(part[p * stride + c0 + c]);
+    }
     sh[g][c] = s;
     __syncthreads();
-    if (g == 0 && c0 + c < cols) store_any(dweight, c0 + c, dtype, static_cast<float>(sh[0][c] + sh[1][c] + sh[2][c] + sh[3][c]));
+    if (g == 0 && c0 + c < cols) {
+      double total = 0.0;
+#pragma unroll
+      for (int q = 0; q < 32; ++q) total += sh[q][c];
+      store_any(dweight, c0 + c, dtype, static_cast<float>(total));
+    }
     __syncthreads();
   }
 }
@@ -442,27 +538,16 @@ __device__ __forceinline__ bf16x8 widen(const V& f, int s, int byte) {
 #define WAIT_VM(v) __builtin_amdgcn_s_waitcnt(((v) & 15) | (7 << 4) | (15 << 8) | (((v) >> 4) << 14))
 #define WAIT_LDS() __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14))
 
-// c[row][col .. col + 8) = v (+ c), the first n of them
-__device__ __forceinline__ void store_row(const MatmulArgs& a, int64_t row, int64_t col, float (&v)[8], bool vec) {
-  const int64_t i = row * a.ldc + col, left = a.b.rows - col;
-  if (vec && left >= 8) {
-    auto put = [&](auto* c) {
-      if (a.accumulate) {
-        float w[8];
-        load8(w, c, 8, true);
+// c[0 .. 8) = v (+ c), the first n of them
+template <typename T>
+__device__ __forceinline__ void put8(T* c, float (&v)[8], int n, int accumulate) {
+  if (accumulate) {
+    float w[8];
+    load8(w, c, n);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += w[e];
-      }
-      store8(c, v, 8, true);
-    };
-    if (a.c_dtype == OKLS_F32) put(static_cast<float*>(a.c) + i);
-    else if (a.c_dtype == OKLS_BF16) put(static_cast<bf16_t*>(a.c) + i);
-    else put(static_cast<half_t*>(a.c) + i);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) store_any(a.c, i + e, a.c_dtype, a.accumulate ? v[e] + load_any(a.c, i + e, a.c_dtype) : v[e]);
+    for (int e = 0; e < 8; ++e) v[e] += w[e];
   }
+  store8(c, v, n);
 }
 
 // A tile of c per workgroup.  The wave's region is GI x GJ blocks of 32 x 32;
@@ -494,8 +579,6 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
   constexpr int H = GI / 2;               // block rows of a phase: a phase is half of a's block rows in one part
   __shared__ __attribute__((aligned(16))) uint8_t sA0[C::BM * 128], sA1[C::BM * 128], sB0[C::BN * 128], sB1[C::BN * 128];
   __shared__ __attribute__((aligned(16))) uint8_t e0[512], e1[512];   // scale bytes of the tile's rows, a's and from 256 on b's
-  constexpr int kEdge = 20;               // floats of a row of 16: 16-byte aligned, spread over the banks
-  __shared__ __attribute__((aligned(16))) float edge[C::NW * 32 * kEdge];
   static_assert(C::BM <= 256 && C::BN <= 256, "one copy holds a side's scales");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
@@ -679,11 +762,12 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
   auto finish = [&]() INLINE {
     if (plan.splits > 1) o.c = a.ws + split * m * np;
     const int64_t r0 = m0 + wm * C::RM, c0 = n0 + wn * C::RN;
-    const int size = o.c_dtype == OKLS_F32 ? 4 : 2;
-    const bool vec = (reinterpret_cast<uintptr_t>(o.c) & 15) == 0 && (o.ldc * size) % 16 == 0 && c0 + C::RN <= n;
-    auto each = [&](auto f) INLINE {
+    const bool inside = c0 + C::RN <= n;
+    auto rows = [&](auto* c) INLINE {
+      auto* at = c + (r0 + r32 * GI) * o.ldc + c0 + 8 * half;
 #pragma unroll
-      for (int i = 0; i < GI; ++i)
+      for (int i = 0; i < GI; ++i) {
+        if (r0 + r32 * GI + i >= m) continue;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float v[8];
@@ -691,52 +775,14 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
           for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int j = 0; j < GJ; ++j) v[e * GJ + j] = acc[i][j][4 * q + e];
-          f(i, q, v);
-        }
-    };
-    auto rows = [&](auto* c) INLINE {
-      auto* at = c + (r0 + r32 * GI) * o.ldc + c0 + 8 * half;
-      each([&](int i, int q, float (&v)[8]) INLINE {
-        if (r0 + r32 * GI + i >= m) return;
-        auto* to = at + i * o.ldc + 16 * q;
-        if (o.accumulate) {
-          float u[8];
-          load8(u, to, 8, true);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += u[e];
-        }
-        store8(to, v, 8, true);
-      });
-    };
-    if (vec) {
-      if (F32 || o.c_dtype == OKLS_F32) rows(static_cast<float*>(o.c));
-      else if (o.c_dtype == OKLS_BF16) rows(static_cast<bf16_t*>(o.c));
-      else rows(static_cast<half_t*>(o.c));
-      return;
-    }
-    // Rows that end inside the region or do not start on 16 bytes: 32 x 16
-    // elements at a time through LDS, so that 16 lanes write neighbours
-    // (single elements straight from the lanes touch 64 rows a store).
-    float* mine = edge + wave * 32 * kEdge;
-    each([&](int i, int q, float (&v)[8]) INLINE {
-      asm volatile("" ::: "memory");
-      *reinterpret_cast<floatx4*>(mine + r32 * kEdge + 8 * half) = floatx4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<floatx4*>(mine + r32 * kEdge + 8 * half + 4) = floatx4{v[4], v[5], v[6], v[7]};
-      WAIT_LDS();
-      asm volatile("" ::: "memory");
-      const int64_t col = c0 + 16 * q + (lane & 15);
-#pragma unroll 2
-      for (int t = 0; t < 8; ++t) {
-        const int r = 4 * t + (lane >> 4);
-        const int64_t row = r0 + r * GI + i;
-        const float x = mine[r * kEdge + (lane & 15)];
-        if (row < m && col < n) {
-          const int64_t to = row * o.ldc + col;
-          store_any(o.c, to, o.c_dtype, o.accumulate ? x + load_any(o.c, to, o.c_dtype) : x);
+          const int left = inside ? 8 : clamp8(n - c0 - 16 * q - 8 * half);
+          put8(at + i * o.ldc + 16 * q, v, left, o.accumulate);
         }
       }
-      WAIT_LDS();
-    });
+    };
+    if (F32 || o.c_dtype == OKLS_F32) rows(static_cast<float*>(o.c));
+    else if (o.c_dtype == OKLS_BF16) rows(static_cast<bf16_t*>(o.c));
+    else rows(static_cast<half_t*>(o.c));
   };
 
   using I0 = std::integral_constant<int, 0>;
@@ -761,17 +807,19 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
 // c = the partial sums of each element, added in the splits' order
 __global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs a, int splits) {
   const int64_t m = a.a.rows, n = a.b.rows, np = (n + 7) & ~int64_t(7);
-  const bool vec = (reinterpret_cast<uintptr_t>(a.c) & 15) == 0 && (a.ldc * (a.c_dtype == OKLS_F32 ? 4 : 2)) % 16 == 0;
   for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * 8; i < m * np; i += gridDim.x * 2048ll) {
     float v[8], u[8];
-    load8(v, a.ws + i, 8, true);
+    load8(v, a.ws + i, 8);
     for (int s = 1; s < splits; ++s) {
-      load8(u, a.ws + s * m * np + i, 8, true);
+      load8(u, a.ws + s * m * np + i, 8);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += u[e];
     }
-    const int64_t row = i / np;
-    store_row(a, row, i - row * np, v, vec);
+    const int64_t row = i / np, col = i - row * np, at = row * a.ldc + col;
+    const int left = clamp8(n - col);
+    if (a.c_dtype == OKLS_F32) put8(static_cast<float*>(a.c) + at, v, left, a.accumulate);
+    else if (a.c_dtype == OKLS_BF16) put8(static_cast<bf16_t*>(a.c) + at, v, left, a.accumulate);
+    else put8(static_cast<half_t*>(a.c) + at, v, left, a.accumulate);
   }
 }
 
@@ -925,32 +973,63 @@ hipError_t launch_quantize(const QuantArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// calls go(T{}) with the element type of dtype
+template <class F>
+static void by_type(int dtype, F go) {
+  if (dtype == OKLS_F32) go(float{});
+  else if (dtype == OKLS_BF16) go(bf16_t{});
+  else go(half_t{});
+}
+// calls go(threads of a row, chunks of 8 a thread holds): a wave while a row's
+// chunks fit eight registers' worth of it, then a workgroup
+template <class F>
+static void by_width(int64_t cols, F go) {
+  auto is = [&](auto thr, auto nc) { go(thr, nc); };
+  using W = std::integral_constant<int, 64>;
+  using B = std::integral_constant<int, 256>;
+  if (cols <= 512) is(W{}, std::integral_constant<int, 1>{});
+  else if (cols <= 1024) is(W{}, std::integral_constant<int, 2>{});
+  else if (cols <= 2048) is(W{}, std::integral_constant<int, 4>{});
+  else if (cols <= 4096) is(B{}, std::integral_constant<int, 2>{});
+  else if (cols <= 8192) is(B{}, std::integral_constant<int, 4>{});
+  else if (cols <= 16384) is(B{}, std::integral_constant<int, 8>{});
+  else is(B{}, std::integral_constant<int, 0>{});
+}
+
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
-  const int grid = blocks_up_to(a.rows, 1 << 20);
-  if (a.out.format == OKLS_E4M3) {
-    if (a.dtype == OKLS_F32) rms_norm_kernel<float, OKLS_E4M3><<<grid, 256, 0, s>>>(a);
-    else if (a.dtype == OKLS_BF16) rms_norm_kernel<bf16_t, OKLS_E4M3><<<grid, 256, 0, s>>>(a);
-    else rms_norm_kernel<half_t, OKLS_E4M3><<<grid, 256, 0, s>>>(a);
-  } else {
-    if (a.dtype == OKLS_F32) rms_norm_kernel<float, OKLS_E5M2><<<grid, 256, 0, s>>>(a);
-    else if (a.dtype == OKLS_BF16) rms_norm_kernel<bf16_t, OKLS_E5M2><<<grid, 256, 0, s>>>(a);
-    else rms_norm_kernel<half_t, OKLS_E5M2><<<grid, 256, 0, s>>>(a);
-  }
+  by_type(a.dtype, [&](auto type) {
+    by_width(a.cols, [&](auto thr, auto nc) {
+      using T = decltype(type);
+      constexpr int THR = decltype(thr)::value, NC = decltype(nc)::value;
+      const int grid = blocks_up_to((a.rows * THR + kThreads - 1) / kThreads, 1 << 20);
+      if (a.out.format == OKLS_E4M3) rms_norm_kernel<T, OKLS_E4M3, THR, NC><<<grid, kThreads, 0, s>>>(a);
+      else rms_norm_kernel<T, OKLS_E5M2, THR, NC><<<grid, kThreads, 0, s>>>(a);
+    });
+  });
   return hipGetLastError();
 }
 
+// Workgroups of the gradient: each leaves a row of partial sums to write and
+// read again, so at least two rows of the matrix go to each.
+static int grad_blocks(int64_t rows, int64_t cols) {
+  const int64_t each = cols <= 2048 ? 8 : 2;
+  return blocks_up_to((rows + each - 1) / each, kGradBlocks);
+}
+
 size_t norm_grad_workspace(int64_t rows, int64_t cols) {
-  return static_cast<size_t>(blocks_up_to(rows, kGradBlocks)) * ((cols + 7) / 8 * 8) * 4;
+  return static_cast<size_t>(grad_blocks(rows, cols)) * ((cols + 7) / 8 * 8) * 4;
 }
 
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s) {
-  const int grid = blocks_up_to(a.rows, kGradBlocks);
+  const int grid = grad_blocks(a.rows, a.cols);
   if (grid > 0) {
-    if (a.dtype == OKLS_F32) norm_grad_kernel<float><<<grid, 256, 0, s>>>(a);
-    else if (a.dtype == OKLS_BF16) norm_grad_kernel<bf16_t><<<grid, 256, 0, s>>>(a);
-    else norm_grad_kernel<half_t><<<grid, 256, 0, s>>>(a);
+    by_type(a.dtype, [&](auto type) {
+      by_width(a.cols, [&](auto thr, auto nc) {
+        norm_grad_kernel<decltype(type), decltype(thr)::value, decltype(nc)::value><<<grid, kThreads, 0, s>>>(a);
+      });
+    });
   }
-  norm_dw_kernel<<<blocks_up_to((a.cols + 63) / 64, 1 << 16), 256, 0, s>>>(a.ws, grid, (a.cols + 7) / 8 * 8, a.cols, a.dweight, a.weight_dtype);
+  norm_dw_kernel<<<blocks_up_to((a.cols + 31) / 32, 1 << 16), 1024, 0, s>>>(a.ws, grid, (a.cols + 7) / 8 * 8, a.cols, a.dweight, a.weight_dtype);
   return hipGetLastError();
 }
 
