@@ -57,25 +57,44 @@ __device__ __forceinline__ void store_any(void* p, int64_t i, int dtype, float v
 // alignment, so rows that start anywhere need no path of their own.
 typedef u16x8 u16x8_any __attribute__((aligned(2)));
 typedef floatx4 floatx4_any __attribute__((aligned(4)));
+// the eight as they lie in memory: four registers for 16-bit types
+template <typename T> struct Raw8 { u16x8 v; };
+template <> struct Raw8<float> { floatx4 a, b; };
 template <typename T>
-__device__ __forceinline__ void load8(float (&v)[8], const T* p, int n) {
-  if (n >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      const floatx4 a = reinterpret_cast<const floatx4_any*>(p)[0], b = reinterpret_cast<const floatx4_any*>(p)[1];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+__device__ __forceinline__ Raw8<T> raw8(const T* p, int n) {
+  Raw8<T> r{};
+  if constexpr (sizeof(T) == 4) {
+    if (n >= 8) {
+      r.a = reinterpret_cast<const floatx4_any*>(p)[0], r.b = reinterpret_cast<const floatx4_any*>(p)[1];
     } else {
-      const u16x8 a = *reinterpret_cast<const u16x8_any*>(p);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (__is_same(T, bf16_t)) v[j] = to_f32(bf16_t{a[j]});
-        else v[j] = to_f32(__builtin_bit_cast(half_t, static_cast<uint16_t>(a[j])));
+      for (int j = 0; j < 4; ++j) {
+        if (j < n) r.a[j] = p[j];
+        if (4 + j < n) r.b[j] = p[4 + j];
       }
     }
   } else {
+    if (n >= 8) {
+      r.v = *reinterpret_cast<const u16x8_any*>(p);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? to_f32(p[j]) : 0.0f;
+      for (int j = 0; j < 8; ++j)
+        if (j < n) r.v[j] = __builtin_bit_cast(uint16_t, p[j]);
+    }
   }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen8(float (&v)[8], const Raw8<T>& r) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (sizeof(T) == 4) v[j] = j < 4 ? r.a[j & 3] : r.b[j & 3];
+    else v[j] = to_f32(__builtin_bit_cast(T, static_cast<uint16_t>(r.v[j])));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void load8(float (&v)[8], const T* p, int n) {
+  widen8(v, raw8(p, n));
 }
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n) {
@@ -248,35 +267,37 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
 // Norm
 // ---------------------------------------------------------------------------
 
-// A row by a wave (THR = 64) or by a workgroup's four (THR = 256), its NC
-// chunks of 8 elements a thread held in registers from the one read of it.
-// Wider rows (NC = 0) are read again for the second pass.
-constexpr int kThreads = 256;
+// A row by a wave (THR = 64, four rows a workgroup) or by a workgroup of as
+// many waves as it fills, THR threads at most; its NC chunks of 8 elements a
+// thread are held in registers from the one read of it.  Wider rows (NC = 0)
+// are read again for the second pass.
+template <int THR> constexpr int kThreads = THR > 64 ? THR : 256;
 
 // the sum of v over a row's threads, in each of them, in a fixed order
 template <int THR, typename V>
 __device__ __forceinline__ V row_sum(V v, V* sh) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  if constexpr (THR == 256) {
+  if constexpr (THR > 64) {
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = sh[0] + sh[1] + sh[2] + sh[3];
+    v = sh[0];
+    for (int q = 1; q < static_cast<int>(blockDim.x >> 6); ++q) v += sh[q];
     __syncthreads();
   }
   return v;
 }
 
 template <typename T, int FMT, int THR, int NC>
-__global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
-  __shared__ double sh[4];
-  constexpr int ROWS = kThreads / THR;
-  const int t = threadIdx.x % THR;
+__global__ __launch_bounds__(kThreads<THR>) void rms_norm_kernel(NormArgs a) {
+  __shared__ double sh[16];
+  constexpr int ROWS = THR == 64 ? 4 : 1;
+  const int thr = THR == 64 ? 64 : blockDim.x, t = THR == 64 ? threadIdx.x % 64 : threadIdx.x;
   const T* x = static_cast<const T*>(a.x);
   const T* res = static_cast<const T*>(a.residual);
   T* hs = static_cast<T*>(a.h);
   const int64_t chunks = ((a.cols + 127) >> 7) * 16;   // whole blocks: past the end v = 0
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / THR; row < a.rows; row += static_cast<int64_t>(gridDim.x) * ROWS) {
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + (THR == 64 ? threadIdx.x / 64 : 0); row < a.rows; row += static_cast<int64_t>(gridDim.x) * ROWS) {
     auto read = [&](float (&v)[8], int64_t c) { load8(v, x + row * a.ldx + c * 8, clamp8(a.cols - c * 8)); };
     auto add = [&](float (&v)[8], int64_t c, bool store) {
       const int n = clamp8(a.cols - c * 8);
@@ -317,25 +338,25 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
     if constexpr (NC != 0) {
       float v[NC][8];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) read(v[i], t + i * THR);      // nothing past the end
+      for (int i = 0; i < NC; ++i) read(v[i], t + i * thr);      // nothing past the end
       if (res != nullptr)
 #pragma unroll
-        for (int i = 0; i < NC; ++i) add(v[i], t + i * THR, true);
+        for (int i = 0; i < NC; ++i) add(v[i], t + i * thr, true);
 #pragma unroll
       for (int i = 0; i < NC; ++i) ss = squares(v[i], ss);
       const float rstd = rms(ss);
 #pragma unroll
       for (int i = 0; i < NC; ++i)
-        if (t + i * THR < chunks) write(v[i], t + i * THR, rstd);
+        if (t + i * thr < chunks) write(v[i], t + i * thr, rstd);
     } else {
       float v[8];
-      for (int64_t c = t; c < chunks; c += THR) {
+      for (int64_t c = t; c < chunks; c += thr) {
         read(v, c);
         if (res != nullptr) add(v, c, true);
         ss = squares(v, ss);
       }
       const float rstd = rms(ss);
-      for (int64_t c = t; c < chunks; c += THR) {
+      for (int64_t c = t; c < chunks; c += thr) {
         read(v, c);
         if (res != nullptr) add(v, c, false);
         write(v, c, rstd);
@@ -344,15 +365,15 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(NormArgs a) {
   }
 }
 
-constexpr int kGradBlocks = 512;   // most blocks of a launch, each with one row of partial sums of dweight
+constexpr int kGradBlocks = 1024;   // most workgroups of a launch, each with one row of partial sums of dweight
 
 // The same layout.  A thread meets the same columns in every row, so dweight's
 // sums stay in its registers; a workgroup leaves one row of partial sums.
 template <typename T, int THR, int NC>
-__global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs a) {
-  constexpr int ROWS = kThreads / THR;
-  __shared__ float sh[4];
-  const int t = threadIdx.x % THR;
+__global__ __launch_bounds__(kThreads<THR>) void norm_grad_kernel(NormGradArgs a) {
+  constexpr int ROWS = THR == 64 ? 4 : 1;
+  __shared__ float sh[16];
+  const int thr = THR == 64 ? 64 : blockDim.x, t = THR == 64 ? threadIdx.x % 64 : threadIdx.x;
   const T* dy = static_cast<const T*>(a.dy);
   const T* h = static_cast<const T*>(a.h);
   const T* dh = static_cast<const T*>(a.dh);
@@ -365,9 +386,7 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs a) {
     for (int j = 0; j < 8; ++j) dot = fmaf(g[j] * w[j], u[j] * rstd, dot);
     return dot;
   };
-  auto finish8 = [&](float (&g)[8], float (&u)[8], const float (&w)[8], float (&sum)[8], float rstd, float mean, int64_t row, int64_t c, int n) {
-    float d[8] = {};
-    if (dh != nullptr) load8(d, dh + row * a.lddh + c * 8, n);
+  auto finish8 = [&](float (&g)[8], float (&u)[8], const float (&w)[8], const float (&d)[8], float (&sum)[8], float rstd, float mean, int64_t row, int64_t c, int n) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float hat = u[j] * rstd;
@@ -379,31 +398,40 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs a) {
   const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
   if constexpr (NC != 0) {
     float sum[NC][8] = {};
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / THR; row < a.rows; row += step) {
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + (THR == 64 ? threadIdx.x / 64 : 0); row < a.rows; row += step) {
+      // as they lie in memory, dh before the reduction too: half the registers,
+      // and every load of the row on its way at once
       const float rstd = a.rstd[row];
-      float g[NC][8], u[NC][8], dot = 0.0f;
+      Raw8<T> g[NC], u[NC], d[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int64_t c = t + i * THR;
+        const int64_t c = t + i * thr;
         const int n = clamp8(a.cols - c * 8);
-        load8(g[i], dy + row * a.lddy + c * 8, n);
-        load8(u[i], h + row * a.ldh + c * 8, n);
+        g[i] = raw8(dy + row * a.lddy + c * 8, n);
+        u[i] = raw8(h + row * a.ldh + c * 8, n);
+        d[i] = dh != nullptr ? raw8(dh + row * a.lddh + c * 8, n) : Raw8<T>{};
       }
+      float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int64_t c = t + i * THR;
-        float w[8];
+        const int64_t c = t + i * thr;
+        float w[8], gf[8], uf[8];
         load8_any(w, a.weight, c * 8, clamp8(a.cols - c * 8), a.weight_dtype);
-        dot = dot8(g[i], u[i], w, rstd, dot);
+        widen8(gf, g[i]);
+        widen8(uf, u[i]);
+        dot = dot8(gf, uf, w, rstd, dot);
       }
       const float mean = row_sum<THR>(dot, sh) * inv;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const int64_t c = t + i * THR;
+        const int64_t c = t + i * thr;
         const int n = clamp8(a.cols - c * 8);
-        float w[8];
+        float w[8], gf[8], uf[8], df[8];
         load8_any(w, a.weight, c * 8, n, a.weight_dtype);
-        finish8(g[i], u[i], w, sum[i], rstd, mean, row, c, n);
+        widen8(gf, g[i]);
+        widen8(uf, u[i]);
+        widen8(df, d[i]);
+        finish8(gf, uf, w, df, sum[i], rstd, mean, row, c, n);
       }
     }
     if constexpr (ROWS > 1) {
@@ -415,7 +443,7 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) joined[me][j][t] = sum[i][j];
         __syncthreads();
-        for (int e = threadIdx.x; e < 8 * THR; e += kThreads) {
+        for (int e = threadIdx.x; e < 8 * THR; e += 256) {
           const int64_t col = static_cast<int64_t>(i) * THR * 8 + e;
           float s = 0.0f;
 #pragma unroll
@@ -427,10 +455,10 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs a) {
     } else {
 #pragma unroll
       for (int i = 0; i < NC; ++i)
-        if (t + i * THR < chunks) store8(part + (t + i * THR) * 8, sum[i], 8);
+        if (t + i * thr < chunks) store8(part + (t + i * thr) * 8, sum[i], 8);
     }
   } else {
-    for (int64_t c = t; c < chunks; c += THR)
+    for (int64_t c = t; c < chunks; c += thr)
 #pragma unroll
       for (int j = 0; j < 8; ++j) part[c * 8 + j] = 0.0f;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -441,16 +469,18 @@ __global__ __launch_bounds__(kThreads) void norm_grad_kernel(NormGradArgs a) {
         load8(u, h + row * a.ldh + c * 8, n);
         load8_any(w, a.weight, c * 8, n, a.weight_dtype);
       };
-      for (int64_t c = t; c < chunks; c += THR) {
+      for (int64_t c = t; c < chunks; c += thr) {
         read(c, clamp8(a.cols - c * 8));
         dot = dot8(g, u, w, rstd, dot);
       }
       const float mean = row_sum<THR>(dot, sh) * inv;
-      for (int64_t c = t; c < chunks; c += THR) {
+      for (int64_t c = t; c < chunks; c += thr) {
         const int n = clamp8(a.cols - c * 8);
         read(c, n);
         load8(sum, part + c * 8, 8);
-        finish8(g, u, w, sum, rstd, mean, row, c, n);
+        float d[8] = {};
+        if (dh != nullptr) load8(d, dh + row * a.lddh + c * 8, n);
+        finish8(g, u, w, d, sum, rstd, mean, row, c, n);
         store8(part + c * 8, sum, 8);
       }
     }
@@ -980,40 +1010,45 @@ static void by_type(int dtype, F go) {
   else if (dtype == OKLS_BF16) go(bf16_t{});
   else go(half_t{});
 }
-// calls go(threads of a row, chunks of 8 a thread holds): a wave while a row's
-// chunks fit eight registers' worth of it, then a workgroup
+// calls go(most threads of a row, chunks of 8 a thread holds, threads of a
+// workgroup).  At most two chunks: more cost the waves that hide the loads (the
+// gradient of 16384 x 2048 takes 63 us with a wave a row, 56 with a workgroup;
+// of 4000 x 16000 176 us with 256 threads of eight chunks, 110 with 1024 of two).
 template <class F>
 static void by_width(int64_t cols, F go) {
-  auto is = [&](auto thr, auto nc) { go(thr, nc); };
-  using W = std::integral_constant<int, 64>;
-  using B = std::integral_constant<int, 256>;
-  if (cols <= 512) is(W{}, std::integral_constant<int, 1>{});
-  else if (cols <= 1024) is(W{}, std::integral_constant<int, 2>{});
-  else if (cols <= 2048) is(W{}, std::integral_constant<int, 4>{});
-  else if (cols <= 4096) is(B{}, std::integral_constant<int, 2>{});
-  else if (cols <= 8192) is(B{}, std::integral_constant<int, 4>{});
-  else if (cols <= 16384) is(B{}, std::integral_constant<int, 8>{});
-  else is(B{}, std::integral_constant<int, 0>{});
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  const int64_t waves = (cols + 511) / 512;        // of one chunk a lane
+  const int one = static_cast<int>(waves) * 64, two = static_cast<int>((waves + 1) / 2) * 64;
+  if (cols <= 512) go(std::integral_constant<int, 64>{}, I1{}, 256);
+  else if (cols <= 1024) go(std::integral_constant<int, 64>{}, I2{}, 256);
+  else if (cols <= 2048) go(std::integral_constant<int, 256>{}, I1{}, one);
+  else if (cols <= 8192) go(std::integral_constant<int, 512>{}, I2{}, two);
+  else if (cols <= 16384) go(std::integral_constant<int, 1024>{}, I2{}, two);
+  else go(std::integral_constant<int, 1024>{}, I0{}, 1024);
 }
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
   by_type(a.dtype, [&](auto type) {
-    by_width(a.cols, [&](auto thr, auto nc) {
+    by_width(a.cols, [&](auto thr, auto nc, int threads) {
       using T = decltype(type);
       constexpr int THR = decltype(thr)::value, NC = decltype(nc)::value;
-      const int grid = blocks_up_to((a.rows * THR + kThreads - 1) / kThreads, 1 << 20);
-      if (a.out.format == OKLS_E4M3) rms_norm_kernel<T, OKLS_E4M3, THR, NC><<<grid, kThreads, 0, s>>>(a);
-      else rms_norm_kernel<T, OKLS_E5M2, THR, NC><<<grid, kThreads, 0, s>>>(a);
+      constexpr int rows = THR == 64 ? 4 : 1;
+      const int grid = blocks_up_to((a.rows + rows - 1) / rows, 1 << 20);
+      if (a.out.format == OKLS_E4M3) rms_norm_kernel<T, OKLS_E4M3, THR, NC><<<grid, threads, 0, s>>>(a);
+      else rms_norm_kernel<T, OKLS_E5M2, THR, NC><<<grid, threads, 0, s>>>(a);
     });
   });
   return hipGetLastError();
 }
 
 // Workgroups of the gradient: each leaves a row of partial sums to write and
-// read again, so at least two rows of the matrix go to each.
+// read again, so at least two of the matrix's rows go to each, and more to the
+// larger workgroups, of which fewer fill the card.
 static int grad_blocks(int64_t rows, int64_t cols) {
-  const int64_t each = cols <= 2048 ? 8 : 2;
-  return blocks_up_to((rows + each - 1) / each, kGradBlocks);
+  const int64_t each = cols <= 1024 ? 8 : 2;
+  return blocks_up_to((rows + each - 1) / each, cols <= 4096 ? kGradBlocks : cols <= 8192 ? kGradBlocks / 2 : kGradBlocks / 4);
 }
 
 size_t norm_grad_workspace(int64_t rows, int64_t cols) {
@@ -1024,8 +1059,8 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s) {
   const int grid = grad_blocks(a.rows, a.cols);
   if (grid > 0) {
     by_type(a.dtype, [&](auto type) {
-      by_width(a.cols, [&](auto thr, auto nc) {
-        norm_grad_kernel<decltype(type), decltype(thr)::value, decltype(nc)::value><<<grid, kThreads, 0, s>>>(a);
+      by_width(a.cols, [&](auto thr, auto nc, int threads) {
+        norm_grad_kernel<decltype(type), decltype(thr)::value, decltype(nc)::value><<<grid, threads, 0, s>>>(a);
       });
     });
   }
