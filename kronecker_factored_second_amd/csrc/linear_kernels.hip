@@ -85,12 +85,14 @@ __device__ __forceinline__ Raw8<T> raw8(const T* p, int n) {
   return r;
 }
 template <typename T>
+__device__ __forceinline__ float element(const Raw8<T>& r, int j) {
+  if constexpr (sizeof(T) == 4) return j < 4 ? r.a[j & 3] : r.b[j & 3];
+  else return to_f32(__builtin_bit_cast(T, static_cast<uint16_t>(r.v[j])));
+}
+template <typename T>
 __device__ __forceinline__ void widen8(float (&v)[8], const Raw8<T>& r) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if constexpr (sizeof(T) == 4) v[j] = j < 4 ? r.a[j & 3] : r.b[j & 3];
-    else v[j] = to_f32(__builtin_bit_cast(T, static_cast<uint16_t>(r.v[j])));
-  }
+  for (int j = 0; j < 8; ++j) v[j] = element(r, j);
 }
 template <typename T>
 __device__ __forceinline__ void load8(float (&v)[8], const T* p, int n) {
@@ -165,14 +167,15 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
 __device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // One 128 x 128 tile per pass, 256 threads: thread t holds rows 8 (t / 16) + p
-// and columns 8 (t % 16) + j.  A row's maximum is over 16 neighbouring lanes, a
-// column's over the four lane groups of a wave and, through LDS, the four
-// waves.  The transposed codes go through LDS so that they leave as whole rows
-// of 128 bytes.
+// and columns 8 (t % 16) + j, as they lie in memory: 16-bit types take half the
+// registers, so more waves hide the loads.  A row's maximum is over 16
+// neighbouring lanes, a column's over the four lane groups of a wave and,
+// through LDS, the four waves.  The transposed codes go through LDS so that
+// they leave as whole rows of 128 bytes.
 constexpr int kTileStride = 128 + 16;   // bytes; 16-byte rows that start at different banks
 
-template <typename T, int FMT>
-__global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
+template <typename T, int FMT, bool FACTORS>
+__global__ __launch_bounds__(256, 4) void quantize_kernel(QuantArgs a) {
   __shared__ uint32_t col_top[4][128];
   __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kTileStride];
   const int t = threadIdx.x, c8 = t & 15, rg = t >> 4, wave = t >> 6;
@@ -182,39 +185,39 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
     const int64_t br = it / tiles_c, bc = it - br * tiles_c;
     const int64_t r0 = br * 128 + rg * 8, c0 = bc * 128 + c8 * 8;
     const int nc = clamp8(a.cols - c0);
-    float v[8][8];
+    Raw8<T> raw[8];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      if (r0 + p < a.rows) load8(v[p], x + (r0 + p) * a.ldx + c0, nc);
-      else
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[p][j] = 0.0f;
-    }
-    if (a.row_factor != nullptr) {
-      float cf[8];
+    for (int p = 0; p < 8; ++p) raw[p] = raw8(x + (r0 + p) * a.ldx + c0, r0 + p < a.rows ? nc : 0);
+    float rf[8], cf[8];
+    if constexpr (FACTORS) {
       load8_any(cf, a.col_factor, c0, nc, a.col_dtype);
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        const float rf = r0 + p < a.rows ? a.row_factor[r0 + p] : 0.0f;
-        // no value past the matrix's end, where 0 times a factor's infinity or NaN would not be 0
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[p][j] = j < nc && r0 + p < a.rows ? v[p][j] * rf * cf[j] : 0.0f;
-      }
+      for (int p = 0; p < 8; ++p) rf[p] = r0 + p < a.rows ? a.row_factor[r0 + p] : 0.0f;
     }
+    auto value = [&](int p, int j) {
+      const float e = element(raw[p], j);
+      // no value past the matrix's end, where 0 times a factor's infinity or NaN would not be 0
+      if constexpr (FACTORS) return j < nc && r0 + p < a.rows ? e * rf[p] * cf[j] : 0.0f;
+      else return e;
+    };
     if (a.along_cols.codes != nullptr) {
       const Blocked& o = a.along_cols;
       uint64_t bytes = 0;
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
         uint32_t top = 0;
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max_u32(top, finite_abs(v[p][j]));
+        for (int j = 0; j < 8; ++j) {
+          v[j] = value(p, j);
+          top = max_u32(top, finite_abs(v[j]));
+        }
 #pragma unroll
         for (int m = 1; m < 16; m <<= 1) top = max_u32(top, __shfl_xor(top, m, 64));
         const uint32_t byte = scale_byte<FMT>(top);
         bytes |= static_cast<uint64_t>(byte) << (8 * p);
         if (r0 + p < a.rows)
-          *reinterpret_cast<uint2*>(o.codes + (r0 + p) * o.ld + c0) = codes8<FMT>(v[p], scale_inverse(byte));
+          *reinterpret_cast<uint2*>(o.codes + (r0 + p) * o.ld + c0) = codes8<FMT>(v, scale_inverse(byte));
       }
       // rows past the end have the scale of zeros; the row stride is padded to 16
       if (c8 == 0 && r0 < o.ld_scale && r0 < ((a.rows + 15) & ~int64_t(15)))
@@ -227,7 +230,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
       for (int j = 0; j < 8; ++j) {
         top[j] = 0;
 #pragma unroll
-        for (int p = 0; p < 8; ++p) top[j] = max_u32(top[j], finite_abs(v[p][j]));
+        for (int p = 0; p < 8; ++p) top[j] = max_u32(top[j], finite_abs(value(p, j)));
         top[j] = max_u32(top[j], __shfl_xor(top[j], 16, 64));
         top[j] = max_u32(top[j], __shfl_xor(top[j], 32, 64));
       }
@@ -245,7 +248,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a) {
         bytes |= static_cast<uint64_t>(byte) << (8 * j);
         float u[8];
 #pragma unroll
-        for (int p = 0; p < 8; ++p) u[p] = v[p][j];
+        for (int p = 0; p < 8; ++p) u[p] = value(p, j);
         *reinterpret_cast<uint2*>(tile + (c8 * 8 + j) * kTileStride + rg * 8) = codes8<FMT>(u, scale_inverse(byte));
       }
       if (rg == 0 && c0 < ((a.cols + 15) & ~int64_t(15)))
@@ -972,6 +975,13 @@ void by_format(const MatmulArgs& a, F go) {
   else second(I1{});
 }
 
+// calls go(T{}) with the element type of dtype
+template <class F>
+void by_type(int dtype, F go) {
+  if (dtype == OKLS_F32) go(float{});
+  else if (dtype == OKLS_BF16) go(bf16_t{});
+  else go(half_t{});
+}
 int blocks_up_to(int64_t n, int most) { return static_cast<int>(n < most ? n : most); }
 
 }  // namespace
@@ -981,15 +991,16 @@ hipError_t launch_quantize(const QuantArgs& a, hipStream_t s) {
   const int grid = blocks_up_to(tiles, 1 << 20);
   // the two outputs may differ in format only by two launches
   auto go = [&](const QuantArgs& q, int fmt) {
-    if (fmt == OKLS_E4M3) {
-      if (q.x_dtype == OKLS_F32) quantize_kernel<float, OKLS_E4M3><<<grid, 256, 0, s>>>(q);
-      else if (q.x_dtype == OKLS_BF16) quantize_kernel<bf16_t, OKLS_E4M3><<<grid, 256, 0, s>>>(q);
-      else quantize_kernel<half_t, OKLS_E4M3><<<grid, 256, 0, s>>>(q);
-    } else {
-      if (q.x_dtype == OKLS_F32) quantize_kernel<float, OKLS_E5M2><<<grid, 256, 0, s>>>(q);
-      else if (q.x_dtype == OKLS_BF16) quantize_kernel<bf16_t, OKLS_E5M2><<<grid, 256, 0, s>>>(q);
-      else quantize_kernel<half_t, OKLS_E5M2><<<grid, 256, 0, s>>>(q);
-    }
+    by_type(q.x_dtype, [&](auto type) {
+      using T = decltype(type);
+      if (q.row_factor != nullptr) {
+        if (fmt == OKLS_E4M3) quantize_kernel<T, OKLS_E4M3, true><<<grid, 256, 0, s>>>(q);
+        else quantize_kernel<T, OKLS_E5M2, true><<<grid, 256, 0, s>>>(q);
+      } else {
+        if (fmt == OKLS_E4M3) quantize_kernel<T, OKLS_E4M3, false><<<grid, 256, 0, s>>>(q);
+        else quantize_kernel<T, OKLS_E5M2, false><<<grid, 256, 0, s>>>(q);
+      }
+    });
   };
   if (a.along_cols.codes != nullptr && a.along_rows.codes != nullptr && a.along_cols.format != a.along_rows.format) {
     QuantArgs one = a, two = a;
@@ -1003,13 +1014,6 @@ hipError_t launch_quantize(const QuantArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// calls go(T{}) with the element type of dtype
-template <class F>
-static void by_type(int dtype, F go) {
-  if (dtype == OKLS_F32) go(float{});
-  else if (dtype == OKLS_BF16) go(bf16_t{});
-  else go(half_t{});
-}
 // calls go(most threads of a row, chunks of 8 a thread holds, threads of a
 // workgroup).  At most two chunks: more cost the waves that hide the loads (the
 // gradient of 16384 x 2048 takes 63 us with a wave a row, 56 with a workgroup;
