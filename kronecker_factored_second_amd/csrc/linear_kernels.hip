@@ -175,7 +175,7 @@ __device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a >
 constexpr int kTileStride = 128 + 16;   // bytes; 16-byte rows that start at different banks
 
 template <typename T, int FMT, bool FACTORS>
-__global__ __launch_bounds__(256, 4) void quantize_kernel(QuantArgs a) {
+__global__ __launch_bounds__(256, FACTORS ? 3 : 4) void quantize_kernel(QuantArgs a) {
   __shared__ uint32_t col_top[4][128];
   __shared__ __attribute__((aligned(16))) uint8_t tile[128 * kTileStride];
   const int t = threadIdx.x, c8 = t & 15, rg = t >> 4, wave = t >> 6;
@@ -594,9 +594,10 @@ struct Tile {
 };
 using TileBig = Tile<2, 4, 4, 2>;     // 256 x 256, 8 waves
 using TileSmall = Tile<2, 2, 2, 2>;   // 128 x 128, 4 waves, two workgroups a CU
+using TileNarrow = Tile<1, 2, 2, 2>;  // 64 x 128, 2 waves, three workgroups a CU
 
 struct MatmulPlan {
-  int big;         // which tile
+  int tile;        // 0 none (the few-rows kernel), 1 narrow, 2 small, 3 big
   int splits;      // of the summed axis
   int tm, tn;      // tiles
 };
@@ -1072,21 +1073,37 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Which tile, and into how many parts the summed axis is cut.
+// Which kernel, and into how many parts the summed axis is cut.  Measured here
+// (us, 16-bit results unless fp32 is said, m x n x k):
+//  - up to 16 rows straight from memory: 16 x 11008 x 4096 13.9, narrow tiles
+//    15.5; more rows read a too often that way (64 x 11008 x 4096: 27.9 against
+//    17.6), except where the whole weight takes no time (17 x 1024 x 1024: 3.3
+//    against 6.4).
+//  - the largest tile that still gives most of the 256 CUs one: 2048 x 5632 x
+//    2048 is 176 big tiles, 29.8 (small 32.4); 2048 x 2048 x 2048 only 64,
+//    26.9 (small 16.1); 256 x 5632 x 2048 88 small ones, 14.7 (narrow 13.2).
+//  - narrow tiles too few for the card split the sum, to about 384 workgroups,
+//    where that pays: a stage of 128 takes about 0.6 us, a split sum 3 us more
+//    and its partial sums' way at 5 TB/s.  48 x 5120 x 13824: 65.5 whole, 20.5
+//    in 6; 256 x 5632 x 2048: 13.2 whole, 19.1 in 2.
 static MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k) {
-  const int64_t blocks = (k + 127) / 128;
   MatmulPlan p{};
-  if (m <= 64) return p;      // no tiles: the few-rows kernel
-  p.tm = static_cast<int>((m + 255) / 256), p.tn = static_cast<int>((n + 255) / 256), p.big = 1, p.splits = 1;
-  if (int64_t(p.tm) * p.tn >= 128) return p;
-  p.big = 0, p.tm = static_cast<int>((m + 127) / 128), p.tn = static_cast<int>((n + 127) / 128);
-  const int64_t tiles = int64_t(p.tm) * p.tn;
-  int64_t s = 512 / tiles;
+  p.splits = 1;
+  if (m <= 16 || (m <= 64 && n * k <= (1 << 23))) return p;
+  auto tiles = [&](int tile, int bm, int bn) {
+    p.tile = tile, p.tm = static_cast<int>((m + bm - 1) / bm), p.tn = static_cast<int>((n + bn - 1) / bn);
+    return static_cast<int64_t>(p.tm) * p.tn;
+  };
+  if (tiles(3, TileBig::BM, TileBig::BN) >= 160) return p;
+  if (tiles(2, TileSmall::BM, TileSmall::BN) >= 160) return p;
+  const int64_t t = tiles(1, TileNarrow::BM, TileNarrow::BN), blocks = (k + 127) / 128;
+  int64_t s = (384 + t / 2) / t;
+  if (s > 12) s = 12;
   if (s > blocks / 4) s = blocks / 4;
-  if (s > 16) s = 16;
-  p.splits = s < 2 ? 1 : static_cast<int>(s);
+  if (s > 1 && 0.6 * static_cast<double>(blocks - blocks / s) > 3.0 + static_cast<double>(m) * n * s * 8 / 5e6) p.splits = static_cast<int>(s);
   return p;
 }
+
 size_t matmul_workspace(int64_t m, int64_t n, int64_t k) {
   if (m == 0 || n == 0 || k == 0) return 0;
   const MatmulPlan p = matmul_plan(m, n, k);
@@ -1101,7 +1118,7 @@ hipError_t launch_matmul(const MatmulArgs& a, hipStream_t s) {
   }
   const MatmulPlan p = matmul_plan(m, n, k);
   // rows of codes 2^24 bytes apart leave no tile's side inside 2^32 bytes
-  if (p.tm == 0 || a.a.ld >= (1 << 24) || a.b.ld >= (1 << 24)) {
+  if (p.tile == 0 || a.a.ld >= (1 << 24) || a.b.ld >= (1 << 24)) {
     by_format(a, [&](auto fa, auto fb, auto f32) {
       constexpr int FA = decltype(fa)::value, FB = decltype(fb)::value;
       constexpr bool F32 = decltype(f32)::value;
@@ -1116,8 +1133,9 @@ hipError_t launch_matmul(const MatmulArgs& a, hipStream_t s) {
   by_format(a, [&](auto fa, auto fb, auto f32) {
     constexpr int FA = decltype(fa)::value, FB = decltype(fb)::value;
     constexpr bool F32 = decltype(f32)::value;
-    if (p.big) matmul_tile_kernel<TileBig, FA, FB, F32><<<tiles, TileBig::NT, 0, s>>>(a, p);
-    else matmul_tile_kernel<TileSmall, FA, FB, F32><<<tiles, TileSmall::NT, 0, s>>>(a, p);
+    if (p.tile == 3) matmul_tile_kernel<TileBig, FA, FB, F32><<<tiles, TileBig::NT, 0, s>>>(a, p);
+    else if (p.tile == 2) matmul_tile_kernel<TileSmall, FA, FB, F32><<<tiles, TileSmall::NT, 0, s>>>(a, p);
+    else matmul_tile_kernel<TileNarrow, FA, FB, F32><<<tiles, TileNarrow::NT, 0, s>>>(a, p);
   });
   if (p.splits > 1) matmul_join_kernel<<<blocks_up_to((m * ((n + 7) / 8) + 255) / 256, 2048), 256, 0, s>>>(a, p.splits);
   return hipGetLastError();
