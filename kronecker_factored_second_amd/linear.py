@@ -20,6 +20,7 @@ the HIP library on the current stream, and there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -40,6 +41,9 @@ class BlockedStruct(ctypes.Structure):
 
 
 _lib = None
+# The same entry points with plain pointer arguments: what the calls below pass
+# is checked by then, and a converted structure pointer costs more than the call.
+_fast = {}
 
 
 def load():
@@ -59,7 +63,11 @@ def load():
     lib.okls_rms_norm_backward_workspace_size.argtypes = [i64, i64]
     lib.okls_rms_norm_backward_workspace_size.restype = sz
     for name in ("okls_quantize", "okls_scaled_matmul", "okls_rms_norm", "okls_rms_norm_backward"):
-        getattr(lib, name).restype = ctypes.c_int
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        _fast[name] = ctypes.CFUNCTYPE(ctypes.c_int, *[vp if t is blk else t for t in fn.argtypes])((name, lib))
+    _matmul_workspace.cache_clear()
+    _norm_workspace.cache_clear()
     _lib = lib
     return lib
 
@@ -77,40 +85,52 @@ class Blocked:
     scales: (ceil(cols / 128), ld_scale) float8_e8m0fnu, [b, r] the scale of block
             b of row r; ld_scale >= rows rounded up to 16 (entries past rows are unused).
     """
-    __slots__ = ("codes", "scales", "shape", "_struct")
+    __slots__ = ("codes", "scales", "shape", "_struct", "_address")
 
     def __init__(self, codes, scales, shape):
         self.codes, self.scales, self.shape = codes, scales, shape
-        self._struct = None
+        self._struct = self._address = None
 
     @staticmethod
     def empty(rows, cols, dtype, device):
         if dtype not in FORMATS:
             raise ValueError(f"8-bit dtype must be float8_e4m3fn or float8_e5m2, got {dtype}")
-        return Blocked(torch.empty((rows, _up(cols, BLOCK)), dtype=dtype, device=device),
-                       torch.empty((-(-cols // BLOCK), _up(rows, 16)), dtype=torch.float8_e8m0fnu, device=device),
-                       (rows, cols))
+        blocks, ld_scale = -(-cols // BLOCK), (rows + 15) // 16 * 16
+        q = Blocked(torch.empty((rows, blocks * BLOCK), dtype=dtype, device=device),
+                    torch.empty((blocks, ld_scale), dtype=torch.float8_e8m0fnu, device=device), (rows, cols))
+        if q.codes.is_cuda:     # nothing to check in what was laid out here
+            q._struct = BlockedStruct(q.codes.data_ptr(), q.scales.data_ptr(), rows, cols, blocks * BLOCK, ld_scale, FORMATS[dtype])
+        return q
 
     def struct(self):
         """The checked C view; kept, so the tensors must not be replaced."""
         s = self._struct
         if s is None:
             c, e, (rows, cols) = self.codes, self.scales, self.shape
-            if c.dtype not in FORMATS or e.dtype != torch.float8_e8m0fnu:
+            fmt = FORMATS.get(c.dtype)
+            if fmt is None or e.dtype != torch.float8_e8m0fnu:
                 raise ValueError(f"codes must be float8_e4m3fn or float8_e5m2 and scales float8_e8m0fnu, got {c.dtype} and {e.dtype}")
-            if c.device != e.device or c.device.type != "cuda":
+            if not c.is_cuda or c.device != e.device:
                 raise ValueError(f"codes on {c.device} and scales on {e.device}: both must be on one GPU")
-            if c.dim() != 2 or e.dim() != 2 or c.shape[0] != rows or c.shape[1] < _up(cols, BLOCK) or \
-                    e.shape[0] != -(-cols // BLOCK) or e.shape[1] < _up(rows, 16):
-                raise ValueError(f"codes {tuple(c.shape)} and scales {tuple(e.shape)} do not hold a matrix of {rows} x {cols}")
-            if (c.numel() and c.stride(1) != 1) or (e.numel() and e.stride(1) != 1):
+            cs, es, blocks = c.shape, e.shape, -(-cols // BLOCK)
+            if len(cs) != 2 or len(es) != 2 or cs[0] != rows or cs[1] < blocks * BLOCK or es[0] != blocks or es[1] < _up(rows, 16):
+                raise ValueError(f"codes {tuple(cs)} and scales {tuple(es)} do not hold a matrix of {rows} x {cols}")
+            (ld, inner), (ld_scale, inner_scale) = c.stride(), e.stride()
+            if (inner != 1 and rows and cs[1]) or (inner_scale != 1 and blocks and es[1]):
                 raise ValueError("codes and scales must be contiguous along their last axis")
-            ld = c.stride(0) if rows > 1 and c.shape[1] else c.shape[1]
-            ld_scale = e.stride(0) if e.shape[0] > 1 and e.shape[1] else e.shape[1]
-            if ld % 16 or ld_scale % 16 or c.data_ptr() % 16 or e.data_ptr() % 16:
+            ld = ld if rows > 1 and cs[1] else cs[1]
+            ld_scale = ld_scale if blocks > 1 and es[1] else es[1]
+            codes, scales = c.data_ptr(), e.data_ptr()
+            if (ld | ld_scale | codes | scales) % 16:
                 raise ValueError("rows of codes and scales must be 16-byte aligned")
-            s = self._struct = BlockedStruct(c.data_ptr(), e.data_ptr(), rows, cols, ld, ld_scale, FORMATS[c.dtype])
+            s = self._struct = BlockedStruct(codes, scales, rows, cols, ld, ld_scale, fmt)
         return s
+
+    def address(self):
+        """The address of the checked C view."""
+        if self._address is None:
+            self._address = ctypes.addressof(self.struct())
+        return self._address
 
     def dequantize(self, dtype=torch.float32):
         """The matrix that codes and scales stand for, in torch operations."""
@@ -130,42 +150,59 @@ def _matrix(name, t, like=None):
     """The row stride of a 2-D GPU tensor of a float dtype, contiguous along its rows."""
     if t.dtype not in DTYPES:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU, got {t.device}")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}, expected {tuple(like.shape)} {like.dtype} on {like.device}")
-    rows, cols = t.shape
-    if cols > 1 and rows and t.stride(1) != 1:
+    if like is not None and (shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} is {tuple(shape)} {t.dtype} on {t.device}, expected {tuple(like.shape)} {like.dtype} on {like.device}")
+    rows, cols = shape
+    ld, inner = t.stride()
+    if cols > 1 and rows and inner != 1:
         raise ValueError(f"{name} must be contiguous along its last axis, strides {t.stride()}")
     if rows <= 1:
         return max(cols, 1)
-    ld = t.stride(0)
     if ld < cols:
         raise ValueError(f"{name}'s rows overlap: strides {t.stride()}")
     return ld
 
 
 def _vector(name, t, n, device):
-    if t.dtype not in DTYPES or t.dim() != 1 or t.shape[0] != n or t.device != device or (n > 1 and t.stride(0) != 1):
+    if t.dtype not in DTYPES or t.shape != (n,) or t.device != device or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous float vector of {n} on {device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream     # current_stream(device).cuda_stream without the Stream object
+
+
+@functools.lru_cache(maxsize=4096)
+def _matmul_workspace(m, n, k):
+    return load().okls_scaled_matmul_workspace_size(m, n, k)
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_workspace(rows, cols):
+    return load().okls_rms_norm_backward_workspace_size(rows, cols)
 
 
 def _call(name, device, *args):
     """One library call on the current stream of `device`."""
-    fn = getattr(_lib or load(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if _lib is None:
+        load()
+    fn, index = _fast[name], device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = fn(*args, _raw_stream(index))
     if st != okls.OKLS_OK:
         raise okls.OKLSError(name, st)
 
 
-def _quantize(x, along_cols, along_rows, row_factor, col_factor):
-    ldx = _matrix("x", x)
+def _quantize(x, along_cols, along_rows, row_factor, col_factor, ldx=None):
+    if ldx is None:
+        ldx = _matrix("x", x)
     rows, cols = x.shape
     if (row_factor is None) != (col_factor is None):
         raise ValueError("row_factor and col_factor come together")
@@ -178,8 +215,8 @@ def _quantize(x, along_cols, along_rows, row_factor, col_factor):
             raise ValueError(f"row_factor must be float32, got {row_factor.dtype}")
         rf, cf, cdt = row_factor.data_ptr(), col_factor.data_ptr(), DTYPES[col_factor.dtype]
     _call("okls_quantize", x.device, x.data_ptr(), DTYPES[x.dtype], rows, cols, ldx, rf, cf, cdt,
-          along_cols.struct() if along_cols is not None else None,
-          along_rows.struct() if along_rows is not None else None)
+          along_cols.address() if along_cols is not None else None,
+          along_rows.address() if along_rows is not None else None)
 
 
 def quantize(x, dtype=torch.float8_e4m3fn, transpose=False, row_factor=None, col_factor=None) -> Blocked:
@@ -187,19 +224,19 @@ def quantize(x, dtype=torch.float8_e4m3fn, transpose=False, row_factor=None, col
     x's rows).  With row_factor (rows, float32) and col_factor (cols), of
     fl32(fl32(x row_factor) col_factor): a norm's output formed again from h,
     rstd and the norm's weight."""
-    _matrix("x", x)
+    ldx = _matrix("x", x)
     rows, cols = x.shape
     q = Blocked.empty(cols, rows, dtype, x.device) if transpose else Blocked.empty(rows, cols, dtype, x.device)
-    _quantize(x, None if transpose else q, q if transpose else None, row_factor, col_factor)
+    _quantize(x, None if transpose else q, q if transpose else None, row_factor, col_factor, ldx)
     return q
 
 
 def quantize_both(x, dtype=torch.float8_e4m3fn, row_factor=None, col_factor=None):
     """The 8-bit forms of x and of its transpose, from one read of x."""
-    _matrix("x", x)
+    ldx = _matrix("x", x)
     rows, cols = x.shape
     q, t = Blocked.empty(rows, cols, dtype, x.device), Blocked.empty(cols, rows, dtype, x.device)
-    _quantize(x, q, t, row_factor, col_factor)
+    _quantize(x, q, t, row_factor, col_factor, ldx)
     return q, t
 
 
@@ -207,10 +244,10 @@ def matmul(a: Blocked, b: Blocked, dtype=torch.bfloat16, out=None, accumulate=Fa
     """a b^T for a (m, k) and b (n, k) in 8 bits: (m, n) of `dtype`, or into
     `out` (of its own dtype); accumulate=True adds to what `out` holds.  Sums are
     fp32, rounded once."""
-    sa, sb = a.struct(), b.struct()
-    m, n, k = sa.rows, sb.rows, sa.cols
+    pa, pb = a.address(), b.address()
+    (m, k), (n, kb) = a.shape, b.shape
     device = a.codes.device
-    if sb.cols != k:
+    if kb != k:
         raise ValueError(f"a is {a.shape} and b is {b.shape}: the second sizes must be equal")
     if b.codes.device != device:
         raise ValueError(f"a is on {device}, b on {b.codes.device}")
@@ -225,9 +262,9 @@ def matmul(a: Blocked, b: Blocked, dtype=torch.bfloat16, out=None, accumulate=Fa
         ldc = _matrix("out", out)
         if tuple(out.shape) != (m, n) or out.device != device:
             raise ValueError(f"out is {tuple(out.shape)} on {out.device}, the product is {(m, n)} on {device}")
-    need = (_lib or load()).okls_scaled_matmul_workspace_size(m, n, k)
+    need = _matmul_workspace(m, n, k)
     ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _call("okls_scaled_matmul", device, sa, sb, out.data_ptr(), DTYPES[out.dtype], ldc, 1 if accumulate else 0,
+    _call("okls_scaled_matmul", device, pa, pb, out.data_ptr(), DTYPES[out.dtype], ldc, 1 if accumulate else 0,
           ws.data_ptr() if need else None, need)
     return out
 
@@ -247,7 +284,7 @@ def rms_norm(x, weight, residual=None, eps=1e-6, dtype=torch.float8_e4m3fn) -> N
     rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
     _call("okls_rms_norm", x.device, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
           DTYPES[x.dtype], rows, cols, weight.data_ptr(), DTYPES[weight.dtype], eps,
-          None if residual is None else h.data_ptr(), ldh, rstd.data_ptr(), q.struct())
+          None if residual is None else h.data_ptr(), ldh, rstd.data_ptr(), q.address())
     return NormOutput(q, h, rstd)
 
 
@@ -265,7 +302,7 @@ def rms_norm_backward(dy, h, rstd, weight, dh=None):
     lddh = _matrix("dh", dh, h) if dh is not None else 0
     dx = torch.empty((rows, cols), dtype=h.dtype, device=h.device)
     dweight = torch.empty(cols, dtype=weight.dtype, device=h.device)
-    need = (_lib or load()).okls_rms_norm_backward_workspace_size(rows, cols)
+    need = _norm_workspace(rows, cols)
     ws = torch.empty(need, dtype=torch.uint8, device=h.device) if need else None
     _call("okls_rms_norm_backward", h.device, dy.data_ptr(), lddy, h.data_ptr(), ldh, rstd.data_ptr(),
           weight.data_ptr(), DTYPES[weight.dtype], None if dh is None else dh.data_ptr(), lddh, DTYPES[h.dtype],
