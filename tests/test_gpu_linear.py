@@ -521,3 +521,89 @@ def test_with_the_optimizer():
         other.step(grads=[g])
         opt.zero_grad()
     assert torch.equal(W.detach(), twin)
+
+
+# ---------------------------------------------------------------------------
+# Every way through the product and the norm that sizes choose
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(2569, 4101, 200), (2600, 4352, 130), (8300, 1300, 1), (1409, 1921, 300), (1280, 2048, 385),
+                                   (40, 2101, 4101), (17, 4096, 2200), (63, 9000, 1000), (65, 130, 8000), (100, 100, 3333), (700, 701, 640)])
+def test_matmul_tiles(m, n, k, kind):
+    """256 and 128 tiles whole and with ragged ends, narrow tiles with the sum whole and split."""
+    a, b = _operands(m, n, k, "e5m2" if k % 2 else "e4m3", "e4m3", key=5)
+    _check_product(linear.matmul(a, b, dtype=FLOATS[kind]), a, b, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(2569, 4101, 140), (1409, 1921, 140), (40, 2101, 4101)])
+def test_matmul_tiles_accumulate_and_strided_output(m, n, k, kind):
+    a, b = _operands(m, n, k, key=6)
+    base = _t(_rng(8).standard_normal((m, n)) * 10, kind)
+    for pad, offset in ((0, 0), (3, 1)):
+        out = _padded(base, pad, offset)
+        whole = out.storage_offset()
+        linear.matmul(a, b, out=out, accumulate=True)
+        _check_product(out, a, b, kind, _n(base))
+        flat = torch.as_strided(out, (m * (n + pad),), (1,), whole)
+        assert (flat.view(m, n + pad)[:, n:] == 7.0).all()
+        assert (torch.as_strided(out, (offset,), (1,), 0) == 7.0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_matmul_far_rows(kind):
+    """Rows of codes 2^24 bytes apart: offsets inside a tile pass 32 bits."""
+    a, b = _operands(130, 70, 300, key=9)
+    codes = torch.empty((130, 1 << 24), dtype=torch.uint8, device="cuda")
+    codes[:, :384] = a.codes.view(torch.uint8)
+    far = linear.Blocked(codes.view(torch.float8_e4m3fn), a.scales, (130, 300))
+    c = linear.matmul(far, b, dtype=FLOATS[kind])
+    _check_product(c, a, b, kind)
+    _check_product(linear.matmul(b, far, dtype=FLOATS[kind]), b, a, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [3, 70, 1300])
+def test_matmul_ends_of_the_scales(m, kind):
+    """Blocks at the lowest scale, 2^-127, and at the highest, times ones that bring them back."""
+    n = 2000 if m == 1300 else 100
+    rng = _rng(m, 17)
+    low = np.ldexp(rng.integers(1, 16, (m, 128)).astype(np.float64), -124)       # normal floats; 15 2^-124 <= 448 2^-127
+    high = np.ldexp(rng.integers(1, 8, (n, 128)).astype(np.float64), 120)
+    a, b = linear.quantize(_t(low)), linear.quantize(_t(high))
+    assert (a.scales.view(torch.uint8)[:, :m] < 8).all()
+    _check_product(linear.matmul(a, b, dtype=FLOATS[kind]), a, b, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [512, 513, 600, 1024, 1025, 1500, 2049, 6000, 8192, 8193, 9001, 16385])
+def test_norm_widths(k, kind):
+    """Each layout of a row over waves, and the widths around where it changes."""
+    m = 37
+    rng = _rng(k, 41)
+    x, r, dy, dh = (_t(_values(rng, m, k), kind) for _ in range(4))
+    w = _t(1 + 0.2 * rng.standard_normal(k), kind)
+    q, h, rstd = linear.rms_norm(x, w, residual=r)
+    want = L.rms(_n(h), np.float64(np.float32(1e-6)))
+    assert (np.abs(_n(rstd) - want) <= want * 2.0 ** -24 * (1 + 2.0 ** -20)).all()
+    _check_blocked(q, L.normed32(_n(h), _n(rstd), _n(w)).astype(np.float64), "e4m3")
+    _check_norm_grads(*linear.rms_norm_backward(dy, h, rstd, w, dh=dh), dy, h, rstd, w, dh, kind, kind)
+
+
+def test_norm_backward_in_place():
+    """dx may be dy or dh, through the C entry: every row is read before it is written."""
+    lib = linear.load()
+    rng = _rng(51)
+    for m, k in ((300, 700), (40, 3000), (9, 20000)):
+        h, dy, dh = (_t(_values(rng, m, k), "bf16") for _ in range(3))
+        w, rstd = _t(1 + 0.2 * rng.standard_normal(k)), _t(L.rms(_n(h), 1e-6))
+        want, wantw = linear.rms_norm_backward(dy, h, rstd, w, dh=dh)
+        need = lib.okls_rms_norm_backward_workspace_size(m, k)
+        for which in range(2):
+            ins = [dy.clone(), dh.clone()]
+            dw, ws = torch.empty_like(w), torch.empty(need, dtype=torch.uint8, device="cuda")
+            st = lib.okls_rms_norm_backward(ins[0].data_ptr(), k, h.data_ptr(), k, rstd.data_ptr(), w.data_ptr(), okls.OKLS_F32, ins[1].data_ptr(), k,
+                                            okls.OKLS_BF16, m, k, ins[which].data_ptr(), k, dw.data_ptr(), ws.data_ptr(), need,
+                                            torch.cuda.current_stream().cuda_stream)
+            assert st == 0 and torch.equal(dw, wantw)
+            assert torch.equal(ins[which], want)
