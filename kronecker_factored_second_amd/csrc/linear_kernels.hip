@@ -165,6 +165,15 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
                codes4<FMT>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
 }
 __device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// the maximum over each 16 neighbouring lanes, in all of them: lane exchanges
+// inside the ALU (pairs, pairs of pairs, mirrored halves, mirrored row)
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  auto other = [](uint32_t x, auto ctrl) { return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), decltype(ctrl)::value, 0xf, 0xf, true)); };
+  v = max_u32(v, other(v, std::integral_constant<int, 0xb1>{}));
+  v = max_u32(v, other(v, std::integral_constant<int, 0x4e>{}));
+  v = max_u32(v, other(v, std::integral_constant<int, 0x141>{}));
+  return max_u32(v, other(v, std::integral_constant<int, 0x140>{}));
+}
 
 // One 128 x 128 tile per pass, 256 threads: thread t holds rows 8 (t / 16) + p
 // and columns 8 (t % 16) + j, as they lie in memory: 16-bit types take half the
@@ -188,17 +197,21 @@ __global__ __launch_bounds__(256, FACTORS ? 3 : 4) void quantize_kernel(QuantArg
     Raw8<T> raw[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) raw[p] = raw8(x + (r0 + p) * a.ldx + c0, r0 + p < a.rows ? nc : 0);
-    float rf[8], cf[8];
+    float made[FACTORS ? 8 : 1][8];
     if constexpr (FACTORS) {
+      float cf[8];
       load8_any(cf, a.col_factor, c0, nc, a.col_dtype);
 #pragma unroll
-      for (int p = 0; p < 8; ++p) rf[p] = r0 + p < a.rows ? a.row_factor[r0 + p] : 0.0f;
+      for (int p = 0; p < 8; ++p) {
+        const float rf = r0 + p < a.rows ? a.row_factor[r0 + p] : 0.0f;
+        // no value past the matrix's end, where 0 times a factor's infinity or NaN would not be 0
+#pragma unroll
+        for (int j = 0; j < 8; ++j) made[p][j] = j < nc && r0 + p < a.rows ? element(raw[p], j) * rf * cf[j] : 0.0f;
+      }
     }
     auto value = [&](int p, int j) {
-      const float e = element(raw[p], j);
-      // no value past the matrix's end, where 0 times a factor's infinity or NaN would not be 0
-      if constexpr (FACTORS) return j < nc && r0 + p < a.rows ? e * rf[p] * cf[j] : 0.0f;
-      else return e;
+      if constexpr (FACTORS) return made[p][j];
+      else return element(raw[p], j);
     };
     if (a.along_cols.codes != nullptr) {
       const Blocked& o = a.along_cols;
@@ -212,8 +225,7 @@ __global__ __launch_bounds__(256, FACTORS ? 3 : 4) void quantize_kernel(QuantArg
           v[j] = value(p, j);
           top = max_u32(top, finite_abs(v[j]));
         }
-#pragma unroll
-        for (int m = 1; m < 16; m <<= 1) top = max_u32(top, __shfl_xor(top, m, 64));
+        top = max16(top);
         const uint32_t byte = scale_byte<FMT>(top);
         bytes |= static_cast<uint64_t>(byte) << (8 * p);
         if (r0 + p < a.rows)
@@ -325,8 +337,7 @@ __global__ __launch_bounds__(kThreads<THR>) void rms_norm_kernel(NormArgs a) {
         v[j] = j < n ? v[j] * rstd * w[j] : 0.0f;
         top = max_u32(top, finite_abs(v[j]));
       }
-#pragma unroll
-      for (int m = 1; m < 16; m <<= 1) top = max_u32(top, __shfl_xor(top, m, 64));
+      top = max16(top);
       const uint32_t byte = scale_byte<FMT>(top);
       *reinterpret_cast<uint2*>(a.out.codes + row * a.out.ld + c * 8) = codes8<FMT>(v, scale_inverse(byte));
       if ((t & 15) == 0) a.out.scales[(c >> 4) * a.out.ld_scale + row] = static_cast<uint8_t>(byte);

@@ -24,6 +24,7 @@ import functools
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import okls
 
@@ -325,6 +326,7 @@ class _NormLinear(torch.autograd.Function):
         return (y, h) if residual is not None else y
 
     @staticmethod
+    @once_differentiable     # the kernels below have no gradients of their own
     def backward(ctx, dy, dh=None):
         h, rstd, norm_weight, wt_codes, wt_scales = ctx.saved_tensors
         need_x, need_r, need_n, need_w = ctx.needs_input_grad[:4]
@@ -356,6 +358,7 @@ class _Linear(torch.autograd.Function):
         return matmul(q, w, dtype=x.dtype)
 
     @staticmethod
+    @once_differentiable     # the kernels below have no gradients of their own
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad[:2]
         saved = ctx.saved_tensors

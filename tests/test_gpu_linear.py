@@ -607,3 +607,19 @@ def test_norm_backward_in_place():
                                             torch.cuda.current_stream().cuda_stream)
             assert st == 0 and torch.equal(dw, wantw)
             assert torch.equal(ins[which], want)
+
+
+def test_example_learns():
+    """The example's stack comes nearer its teacher, by the same losses every time."""
+    from examples import train_8bit_mlp
+    losses = train_8bit_mlp.train(steps=12, blocks=2, d=128, f=192, tokens=200)
+    assert np.isfinite(losses).all() and np.mean(losses[-3:]) < np.mean(losses[:3])
+    assert losses == train_8bit_mlp.train(steps=12, blocks=2, d=128, f=192, tokens=200)
+
+
+def test_no_second_derivative():
+    """A gradient of a gradient is refused, not taken as zero."""
+    x, W = torch.randn(8, 128, device="cuda").requires_grad_(), torch.randn(16, 128, device="cuda").requires_grad_()
+    (g,) = torch.autograd.grad(linear.scaled_linear(x, W).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(g.sum(), W)
