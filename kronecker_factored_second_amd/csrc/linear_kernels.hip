@@ -863,7 +863,7 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
         for (int i = 0; i < IP; ++i)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            T v[8];
+            __attribute__((aligned(16))) T v[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -888,7 +888,7 @@ __global__ __launch_bounds__(C::NT, 2) void matmul_tile_kernel(MatmulArgs a, Mat
             if constexpr (sizeof(T) == 4) __builtin_nontemporal_store(__builtin_bit_cast(floatx4, x), reinterpret_cast<floatx4_any*>(to));
             else __builtin_nontemporal_store(__builtin_bit_cast(u16x8, x), reinterpret_cast<u16x8_any*>(to));
           } else {
-            T v[E];
+            __attribute__((aligned(16))) T v[E];
             *reinterpret_cast<intx4*>(v) = x;
 #pragma unroll
             for (int e = 0; e < E; ++e)
@@ -961,7 +961,7 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs a, int spli
 constexpr int kFewWaves = 8;
 template <int TM, int TN, int FA, int FB, bool F32>
 __global__ __launch_bounds__(kFewWaves * 64) void matmul_few_kernel(MatmulArgs a) {
-  constexpr int U = TM * 1 + TN <= 3 ? 4 : 2;    // blocks of k in flight
+  constexpr int U = TM + TN <= 3 ? 4 : 2;        // blocks of k a wave has in flight
   __shared__ floatx4 part[kFewWaves][TM * TN][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t m = a.a.rows, n = a.b.rows, blocks = (a.a.cols + 127) >> 7;
@@ -1220,10 +1220,18 @@ hipError_t launch_matmul(const MatmulArgs& a, hipStream_t s) {
     by_format(a, [&](auto fa, auto fb, auto f32) {
       constexpr int FA = decltype(fa)::value, FB = decltype(fb)::value;
       constexpr bool F32 = decltype(f32)::value;
-      const unsigned one = static_cast<unsigned>((n + 15) / 16), two = static_cast<unsigned>((n + 31) / 32);
-      if (m <= 16) matmul_few_kernel<1, 1, FA, FB, F32><<<one, kFewWaves * 64, 0, s>>>(a);
-      else if (m <= 32) matmul_few_kernel<2, 1, FA, FB, F32><<<one, kFewWaves * 64, 0, s>>>(a);
-      else matmul_few_kernel<4, 2, FA, FB, F32><<<dim3(two, static_cast<unsigned>((m + 63) / 64)), kFewWaves * 64, 0, s>>>(a);
+      // parts of at most 2^21 x 2^24: a launch holds fewer than 2^32 threads and 2^16 workgroups along y
+      for (int64_t m0 = 0; m0 < m; m0 += 1 << 21)
+        for (int64_t n0 = 0; n0 < n; n0 += 1 << 24) {
+          MatmulArgs p = a;
+          p.a.codes += m0 * a.a.ld, p.a.scales += m0, p.a.rows = m - m0 < (1 << 21) ? m - m0 : 1 << 21;
+          p.b.codes += n0 * a.b.ld, p.b.scales += n0, p.b.rows = n - n0 < (1 << 24) ? n - n0 : 1 << 24;
+          p.c = static_cast<uint8_t*>(a.c) + (m0 * a.ldc + n0) * (F32 ? 4 : 2);
+          const unsigned one = static_cast<unsigned>((p.b.rows + 15) / 16), two = static_cast<unsigned>((p.b.rows + 31) / 32);
+          if (m <= 16) matmul_few_kernel<1, 1, FA, FB, F32><<<one, kFewWaves * 64, 0, s>>>(p);
+          else if (m <= 32) matmul_few_kernel<2, 1, FA, FB, F32><<<one, kFewWaves * 64, 0, s>>>(p);
+          else matmul_few_kernel<4, 2, FA, FB, F32><<<dim3(two, static_cast<unsigned>((p.a.rows + 63) / 64)), kFewWaves * 64, 0, s>>>(p);
+        }
     });
     return hipGetLastError();
   }

@@ -623,3 +623,16 @@ def test_no_second_derivative():
     (g,) = torch.autograd.grad(linear.scaled_linear(x, W).square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError):
         torch.autograd.grad(g.sum(), W)
+
+
+def test_matmul_more_columns_than_a_launch():
+    """2^24 columns are more 16-column groups than one launch of the few-rows kernel takes."""
+    n = (1 << 24) + 40
+    a = linear.quantize(_t(_rng(61).integers(1, 8, (1, 8))))
+    b = linear.Blocked.empty(n, 8, torch.float8_e4m3fn, "cuda")
+    b.scales.view(torch.uint8).fill_(127)
+    b.codes.view(torch.uint8).zero_()
+    b.codes[:, 0] = (torch.arange(n, device="cuda") % 13).float().to(torch.float8_e4m3fn)
+    c = linear.matmul(a, b, dtype=torch.float32)
+    want = a.dequantize()[0, 0] * (torch.arange(n, device="cuda") % 13).float()
+    assert torch.equal(c[0], want)          # small whole numbers: nothing rounds
