@@ -377,7 +377,10 @@ class _Linear(torch.autograd.Function):
 
 def _rows(t):
     """A gradient as autograd hands it over may be expanded or transposed; the kernels read rows."""
-    if t is None or t.shape[1] <= 1 or (t.stride(1) == 1 and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1])):
+    if t is None:
+        return t
+    rows, cols = t.shape
+    if (cols <= 1 or t.stride(1) == 1) and (rows <= 1 or t.stride(0) >= cols):
         return t
     return t.contiguous()
 

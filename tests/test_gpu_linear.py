@@ -636,3 +636,29 @@ def test_matmul_more_columns_than_a_launch():
     c = linear.matmul(a, b, dtype=torch.float32)
     want = a.dequantize()[0, 0] * (torch.arange(n, device="cuda") % 13).float()
     assert torch.equal(c[0], want)          # small whole numbers: nothing rounds
+
+
+@pytest.mark.parametrize("m", [1, 5, 70])
+def test_gradient_of_one_column(m):
+    """A layer of one output column (a value or reward head), and a stream of one: gradients that a sum's backward expands have a row stride of zero."""
+    rng = _rng(m, 89)
+    x, W, nw = _t(_values(rng, m, 300), "bf16"), _t(0.05 * rng.standard_normal((1, 300))), _t(1 + 0.2 * rng.standard_normal(300))
+    for f in (lambda a, b: linear.scaled_linear(a, b), lambda a, b: linear.rms_norm_linear(a, nw, b)[0],
+              lambda a, b: linear.rms_norm_linear(a, nw, b, residual=x)[0]):
+        got, want = [], []
+        for grads, back in ((got, lambda y: y.sum().backward()), (want, lambda y: y.backward(torch.ones_like(y)))):
+            a, b = x.clone().requires_grad_(), W.clone().requires_grad_()
+            back(f(a, b))
+            grads += [a.grad, b.grad]
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    # a residual stream of one column, its gradient expanded as well
+    s, w1, V = _t(_values(rng, m, 1), "bf16"), _t([1.5]), _t(rng.standard_normal((20, 1)))
+
+    def grads(back):
+        a, r = s.clone().requires_grad_(), s.clone().requires_grad_()
+        back(linear.rms_norm_linear(a, w1, V, residual=r))
+        return a.grad, r.grad
+
+    got = grads(lambda yh: torch.autograd.backward(yh, (torch.ones_like(yh[0]), torch.ones(1, dtype=torch.bfloat16, device="cuda").expand(m, 1))))
+    want = grads(lambda yh: torch.autograd.backward(yh, [torch.ones_like(t) for t in yh]))
+    assert all(torch.equal(p, q) for p, q in zip(got, want))

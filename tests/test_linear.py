@@ -235,3 +235,16 @@ def test_empty_blocked_and_dequantize():
     q.codes[:, :300] = torch.from_numpy(codes).to(torch.float8_e5m2)
     q.scales[:, :5] = torch.from_numpy(scales).to(torch.float8_e8m0fnu)
     assert np.array_equal(q.dequantize(torch.float64).numpy(), L.dequantize(codes, scales))
+
+
+@pytest.mark.parametrize("m,n", [(1, 1), (5, 1), (0, 1), (1, 4), (5, 4), (5, 0)])
+def test_gradients_reach_the_kernels_as_rows(m, n):
+    """Any layout in which autograd hands a gradient over: expanded, transposed, strided, as it lies; one column is no exception."""
+    base = torch.arange(2.0 * (m + 1) * (n + 3)).reshape(2 * (m + 1), n + 3)
+    for t in (torch.ones(1).expand(m, n), base[:m, :n], base[:2 * m:2, :n], base.T[:n, :m].T, base[:1, :n].expand(m, n),
+              torch.ones(m, 1).expand(m, n)):
+        got = linear._rows(t)
+        assert torch.equal(got, t)
+        assert (n <= 1 or got.stride(1) == 1) and (m <= 1 or got.stride(0) >= n)
+    whole = torch.zeros(m, n + 3)[:, :n]
+    assert linear._rows(whole) is whole and linear._rows(None) is None      # nothing is copied that need not be
