@@ -80,7 +80,9 @@ okls_status okls_scaled_matmul(const okls_blocked* a, const okls_blocked* b, voi
  *   rstd = (mean(h^2) + eps)^-1/2, summed in fp64 and rounded once to fp32,
  *   out  = the 8-bit form of fl32(fl32(h rstd) weight).
  * The statistics in fp64 keep the codes independent of the order of summation.
- * x, residual and h are of `dtype`; weight (cols) of weight_dtype; rstd (rows). */
+ * x, residual and h are of `dtype`; weight (cols) of weight_dtype; rstd (rows).
+ * h may be x or residual (same pointer and stride): the addition in place, at
+ * every width.  Nothing else that is written may overlap anything. */
 okls_status okls_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t dtype,
                           int64_t rows, int64_t cols, const void* weight, int32_t weight_dtype, float eps,
                           void* h, int64_t ldh, float* rstd, const okls_blocked* out, void* stream);

@@ -322,13 +322,13 @@ __global__ __launch_bounds__(kThreads<THR>) void rms_norm_kernel(NormArgs a) {
   const int64_t chunks = ((a.cols + 127) >> 7) * 16;   // whole blocks: past the end v = 0
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + (THR == 64 ? threadIdx.x / 64 : 0); row < a.rows; row += static_cast<int64_t>(gridDim.x) * ROWS) {
     auto read = [&](float (&v)[8], int64_t c) { load8(v, x + row * a.ldx + c * 8, clamp8(a.cols - c * 8)); };
-    auto add = [&](float (&v)[8], int64_t c, bool store) {
+    auto add = [&](float (&v)[8], int64_t c) {
       const int n = clamp8(a.cols - c * 8);
       float r[8];
       load8(r, res + row * a.ldr + c * 8, n);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = to_f32(from_f32<T>(v[j] + r[j]));
-      if (store) store8(hs + row * a.ldh + c * 8, v, n);
+      store8(hs + row * a.ldh + c * 8, v, n);
     };
     auto squares = [&](const float (&v)[8], double ss) {
 #pragma unroll
@@ -363,7 +363,7 @@ __global__ __launch_bounds__(kThreads<THR>) void rms_norm_kernel(NormArgs a) {
       for (int i = 0; i < NC; ++i) read(v[i], t + i * thr);      // nothing past the end
       if (res != nullptr)
 #pragma unroll
-        for (int i = 0; i < NC; ++i) add(v[i], t + i * thr, true);
+        for (int i = 0; i < NC; ++i) add(v[i], t + i * thr);
 #pragma unroll
       for (int i = 0; i < NC; ++i) ss = squares(v[i], ss);
       const float rstd = rms(ss);
@@ -374,13 +374,14 @@ __global__ __launch_bounds__(kThreads<THR>) void rms_norm_kernel(NormArgs a) {
       float v[8];
       for (int64_t c = t; c < chunks; c += thr) {
         read(v, c);
-        if (res != nullptr) add(v, c, true);
+        if (res != nullptr) add(v, c);
         ss = squares(v, ss);
       }
       const float rstd = rms(ss);
+      // the sum from where this thread put it: x or the residual may be the same memory
       for (int64_t c = t; c < chunks; c += thr) {
-        read(v, c);
-        if (res != nullptr) add(v, c, false);
+        if (res != nullptr) load8(v, hs + row * a.ldh + c * 8, clamp8(a.cols - c * 8));
+        else read(v, c);
         write(v, c, rstd);
       }
     }

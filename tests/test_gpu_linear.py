@@ -662,3 +662,25 @@ def test_gradient_of_one_column(m):
     got = grads(lambda yh: torch.autograd.backward(yh, (torch.ones_like(yh[0]), torch.ones(1, dtype=torch.bfloat16, device="cuda").expand(m, 1))))
     want = grads(lambda yh: torch.autograd.backward(yh, [torch.ones_like(t) for t in yh]))
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def _bits(q):
+    return q.codes.view(torch.uint8), q.scales.view(torch.uint8)[:, :q.shape[0]]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("m,k", [(9, 700), (5, 1000), (5, 4096), (3, 16384), (3, 16385), (3, 16391), (2, 40000)])
+def test_rms_norm_in_place(m, k, kind):
+    """h may be x or the residual, through the C entry: rows that are read once and rows that are read again."""
+    lib = linear.load()
+    rng = _rng(m, k, 52)
+    x, r, w = _t(_values(rng, m, k), kind), _t(_values(rng, m, k), kind), _t(1 + 0.2 * rng.standard_normal(k))
+    want = linear.rms_norm(x, w, residual=r)
+    for which in range(2):
+        ins = [x.clone(), r.clone()]
+        q, rstd = linear.Blocked.empty(m, k, F8["e4m3"], x.device), torch.empty(m, device="cuda")
+        dt = linear.DTYPES[x.dtype]
+        st = lib.okls_rms_norm(ins[0].data_ptr(), k, ins[1].data_ptr(), k, dt, m, k, w.data_ptr(), okls.OKLS_F32, 1e-6, ins[which].data_ptr(), k,
+                               rstd.data_ptr(), q.struct(), torch.cuda.current_stream().cuda_stream)
+        assert st == 0 and torch.equal(ins[which], want.h) and torch.equal(rstd, want.rstd)
+        assert all(torch.equal(p, o) for p, o in zip(_bits(q), _bits(want.q)))
