@@ -175,6 +175,7 @@ def _vector(name, t, n, device):
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream     # current_stream(device).cuda_stream without the Stream object
+_written = torch.autograd.graph.increment_version    # tells autograd of a write that went through data_ptr
 
 
 @functools.lru_cache(maxsize=4096)
@@ -252,7 +253,8 @@ def matmul(a: Blocked, b: Blocked, dtype=torch.bfloat16, out=None, accumulate=Fa
         raise ValueError(f"a is {a.shape} and b is {b.shape}: the second sizes must be equal")
     if b.codes.device != device:
         raise ValueError(f"a is on {device}, b on {b.codes.device}")
-    if out is None:
+    given = out is not None
+    if not given:
         if accumulate:
             raise ValueError("accumulate needs out")
         if dtype not in DTYPES:
@@ -263,10 +265,14 @@ def matmul(a: Blocked, b: Blocked, dtype=torch.bfloat16, out=None, accumulate=Fa
         ldc = _matrix("out", out)
         if tuple(out.shape) != (m, n) or out.device != device:
             raise ValueError(f"out is {tuple(out.shape)} on {out.device}, the product is {(m, n)} on {device}")
+        if out.requires_grad and torch.is_grad_enabled():
+            raise ValueError("out requires a gradient, and this product has none: write to it under torch.no_grad()")
     need = _matmul_workspace(m, n, k)
     ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     _call("okls_scaled_matmul", device, pa, pb, out.data_ptr(), DTYPES[out.dtype], ldc, 1 if accumulate else 0,
           ws.data_ptr() if need else None, need)
+    if given:       # a graph that kept it has to know, as of torch's own writes
+        _written((out,))
     return out
 
 

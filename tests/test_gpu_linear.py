@@ -684,3 +684,37 @@ def test_rms_norm_in_place(m, k, kind):
                                rstd.data_ptr(), q.struct(), torch.cuda.current_stream().cuda_stream)
         assert st == 0 and torch.equal(ins[which], want.h) and torch.equal(rstd, want.rstd)
         assert all(torch.equal(p, o) for p, o in zip(_bits(q), _bits(want.q)))
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("m", [8, 70, 300])
+def test_out_is_seen_by_autograd(m, accumulate):
+    """A buffer that a graph keeps and a product then overwrites: the graph's backward raises, as after torch's own writes."""
+    a, b = linear.quantize(torch.ones(m, 128, device="cuda")), linear.quantize(torch.ones(16, 128, device="cuda"))
+    out, x = torch.ones(m, 16, device="cuda"), torch.ones(m, 16, device="cuda").requires_grad_()
+    y = (x * out).sum()                             # keeps out for x's gradient
+    view = out[:, :8]
+    linear.matmul(a, b, out=out, accumulate=accumulate)
+    assert out._version > 0 and view._version == out._version
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    fresh = (x * out).sum()                         # what is kept after the write is right
+    fresh.backward()
+    assert torch.equal(x.grad, out)
+
+
+def test_out_that_requires_a_gradient():
+    """Refused where autograd records, as torch does for out=; taken where it does not."""
+    a, b = linear.quantize(torch.ones(8, 128, device="cuda")), linear.quantize(torch.ones(16, 128, device="cuda"))
+    leaf = torch.zeros(8, 16, device="cuda").requires_grad_()
+    for out in (leaf, leaf * 2):
+        before = out.detach().clone()
+        with pytest.raises(ValueError, match="no_grad"):
+            linear.matmul(a, b, out=out)
+        assert torch.equal(out.detach(), before)
+        with torch.no_grad():
+            linear.matmul(a, b, out=out, accumulate=True)
+        assert torch.equal(out.detach(), before + 128)
+    with torch.inference_mode():                    # its tensors have no version
+        out = torch.empty(8, 16, device="cuda")
+        assert (linear.matmul(a, b, out=out) == 128).all()
