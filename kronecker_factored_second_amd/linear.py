@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from typing import NamedTuple
 
 import torch
@@ -86,11 +87,17 @@ class Blocked:
     scales: (ceil(cols / 128), ld_scale) float8_e8m0fnu, [b, r] the scale of block
             b of row r; ld_scale >= rows rounded up to 16 (entries past rows are unused).
     """
-    __slots__ = ("codes", "scales", "shape", "_struct", "_address")
+    __slots__ = ("_codes", "_scales", "_shape", "_struct", "_address", "_at")
 
     def __init__(self, codes, scales, shape):
-        self.codes, self.scales, self.shape = codes, scales, shape
-        self._struct = self._address = None
+        rows, cols = shape
+        self._codes, self._scales, self._shape = codes, scales, (operator.index(rows), operator.index(cols))
+        self._struct = self._address = self._at = None
+
+    # read-only: another tensor or shape is another Blocked
+    codes = property(operator.attrgetter("_codes"))
+    scales = property(operator.attrgetter("_scales"))
+    shape = property(operator.attrgetter("_shape"))
 
     @staticmethod
     def empty(rows, cols, dtype, device):
@@ -99,15 +106,20 @@ class Blocked:
         blocks, ld_scale = -(-cols // BLOCK), (rows + 15) // 16 * 16
         q = Blocked(torch.empty((rows, blocks * BLOCK), dtype=dtype, device=device),
                     torch.empty((blocks, ld_scale), dtype=torch.float8_e8m0fnu, device=device), (rows, cols))
-        if q.codes.is_cuda:     # nothing to check in what was laid out here
-            q._struct = BlockedStruct(q.codes.data_ptr(), q.scales.data_ptr(), rows, cols, blocks * BLOCK, ld_scale, FORMATS[dtype])
+        if q._codes.is_cuda:    # nothing to check in what was laid out here
+            q._view(q._codes.data_ptr(), q._scales.data_ptr(), blocks * BLOCK, ld_scale, FORMATS[dtype])
         return q
 
+    def _view(self, codes, scales, ld, ld_scale, fmt):
+        self._struct = BlockedStruct(codes, scales, *self._shape, ld, ld_scale, fmt)
+        self._address, self._at = ctypes.addressof(self._struct), (codes, scales)
+
     def struct(self):
-        """The checked C view; kept, so the tensors must not be replaced."""
-        s = self._struct
-        if s is None:
-            c, e, (rows, cols) = self.codes, self.scales, self.shape
+        """The checked C view, kept for as long as both tensors stay where they are."""
+        c, e = self._codes, self._scales
+        codes, scales = c.data_ptr(), e.data_ptr()
+        if self._at != (codes, scales):
+            rows, cols = self._shape
             fmt = FORMATS.get(c.dtype)
             if fmt is None or e.dtype != torch.float8_e8m0fnu:
                 raise ValueError(f"codes must be float8_e4m3fn or float8_e5m2 and scales float8_e8m0fnu, got {c.dtype} and {e.dtype}")
@@ -121,16 +133,14 @@ class Blocked:
                 raise ValueError("codes and scales must be contiguous along their last axis")
             ld = ld if rows > 1 and cs[1] else cs[1]
             ld_scale = ld_scale if blocks > 1 and es[1] else es[1]
-            codes, scales = c.data_ptr(), e.data_ptr()
             if (ld | ld_scale | codes | scales) % 16:
                 raise ValueError("rows of codes and scales must be 16-byte aligned")
-            s = self._struct = BlockedStruct(codes, scales, rows, cols, ld, ld_scale, fmt)
-        return s
+            self._view(codes, scales, ld, ld_scale, fmt)
+        return self._struct
 
     def address(self):
         """The address of the checked C view."""
-        if self._address is None:
-            self._address = ctypes.addressof(self.struct())
+        self.struct()
         return self._address
 
     def dequantize(self, dtype=torch.float32):

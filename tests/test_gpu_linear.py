@@ -718,3 +718,22 @@ def test_out_that_requires_a_gradient():
     with torch.inference_mode():                    # its tensors have no version
         out = torch.empty(8, 16, device="cuda")
         assert (linear.matmul(a, b, out=out) == 128).all()
+
+
+@pytest.mark.parametrize("which", ["codes", "scales"])
+def test_blocked_tensor_moved_in_place(which):
+    """A product reads an operand's tensors where they are at the call, after .data or set_ too."""
+    a, b = _operands(20, 30, 300, key=12)
+    want = linear.matmul(a, b, dtype=torch.float32)
+    t = getattr(a, which)
+    old = t.detach()                                    # the former memory stays allocated
+    fresh = torch.zeros_like(t.view(torch.uint8))       # zero codes, or scales of 2^-127
+    t.data = fresh.view(t.dtype)
+    now = linear.matmul(a, b, dtype=torch.float32)
+    assert not torch.equal(now, want)
+    _check_product(now, a, b, "f32")
+    t.set_(old)
+    assert torch.equal(linear.matmul(a, b, dtype=torch.float32), want)
+    t.set_(old[:1].clone())                             # and checked there: too few rows
+    with pytest.raises(ValueError):
+        linear.matmul(a, b)

@@ -248,3 +248,29 @@ def test_gradients_reach_the_kernels_as_rows(m, n):
         assert (n <= 1 or got.stride(1) == 1) and (m <= 1 or got.stride(0) >= n)
     whole = torch.zeros(m, n + 3)[:, :n]
     assert linear._rows(whole) is whole and linear._rows(None) is None      # nothing is copied that need not be
+
+
+def test_blocked_is_fixed():
+    """Its tensors and shape cannot be replaced under the C view that is kept of them, nor changed through the caller's list."""
+    shape = [5, 300]
+    q = linear.Blocked(torch.zeros(5, 384).to(torch.float8_e4m3fn), torch.ones(3, 16).to(torch.float8_e8m0fnu), shape)
+    for name, other in (("codes", q.codes.clone()), ("scales", q.scales.clone()), ("shape", (4, 300))):
+        with pytest.raises(AttributeError):
+            setattr(q, name, other)
+    shape[0] = 500
+    assert q.shape == (5, 300)
+    with pytest.raises(TypeError):
+        linear.Blocked(q.codes, q.scales, (5, 300.5))
+
+
+def test_blocked_view_follows_its_tensors():
+    """A tensor that was moved in place (set_, .data) is checked again and read where it is.  The first view is set as the kernels' outputs have it."""
+    q = linear.Blocked.empty(5, 300, torch.float8_e4m3fn, "cpu")
+    q._view(q.codes.data_ptr(), q.scales.data_ptr(), 384, 16, 0)
+    first = q.struct()
+    assert q.struct() is first and q.address() == ctypes.addressof(first)
+    q.codes.data = q.codes.clone()
+    with pytest.raises(ValueError, match="GPU"):        # checked anew: these tensors are on the CPU
+        q.struct()
+    with pytest.raises(ValueError, match="GPU"):
+        q.address()
