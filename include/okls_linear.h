@@ -64,9 +64,13 @@ okls_status okls_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t 
  * 8 bits and of equal cols; c is (m, n) of okls_dtype c_dtype with row stride
  * ldc.  Sums are held in fp32 and rounded once to c's type.  16-bit results take
  * the 8-bit matrix instructions, which drop what lies below 2^-13 of the largest
- * of each eight products (about 1.6e-5 of a result in norm, a hundredth of bf16's
- * own rounding); fp32 results take products of the exact values, whose sums
- * round as fp32's.  k = 0 gives zeros.  The workspace (16-byte aligned) holds
+ * of each eight products: about 1.6e-5 of a result in norm, a hundredth of bf16's
+ * own rounding, but up to 2^-10 of the sum of the products' sizes in an element
+ * whose large products cancel.  fp32 results take products of the exact values,
+ * whose sums round as fp32's; a value below 2^-126 may count as zero there, and
+ * one of 2^128, to which the 8-bit form rounds inputs next to fp32's largest, is
+ * an infinity.  A caller to whom 16-bit results drop too much takes fp32 ones and
+ * casts.  k = 0 gives zeros.  The workspace (16-byte aligned) holds
  * partial sums where the summed axis is split over workgroups; it may be NULL
  * where the size is 0. */
 size_t okls_scaled_matmul_workspace_size(int64_t m, int64_t n, int64_t k);

@@ -15,7 +15,9 @@ the HIP library on the current stream, and there is no fallback.
                 dtype=torch.float32)                        # the optimizer's G
     dx, dnorm = rms_norm_backward(dv, h, rstd, norm_weight, dh=dh)
 
-`rms_norm_linear` and `scaled_linear` are these calls as autograd operators.
+`rms_norm_linear` and `scaled_linear` are these calls as autograd operators.  The
+single calls record nothing: their results carry no gradient back to inputs that
+require one.
 """
 from __future__ import annotations
 
@@ -254,8 +256,14 @@ def quantize_both(x, dtype=torch.float8_e4m3fn, row_factor=None, col_factor=None
 
 def matmul(a: Blocked, b: Blocked, dtype=torch.bfloat16, out=None, accumulate=False):
     """a b^T for a (m, k) and b (n, k) in 8 bits: (m, n) of `dtype`, or into
-    `out` (of its own dtype); accumulate=True adds to what `out` holds.  Sums are
-    fp32, rounded once."""
+    `out` (of its own dtype); accumulate=True adds to what `out` holds.
+
+    A float32 result sums the exact products in fp32.  A 16-bit result is summed
+    in fp32 and rounded once, but from each eight products the 8-bit matrix
+    instructions drop what lies below 2^-13 of the largest of them: about 1.6e-5
+    of a result in norm, up to 2^-10 of the sum of the products' sizes in an
+    element whose large products cancel.  Where that counts, take a float32
+    result and cast it."""
     pa, pb = a.address(), b.address()
     (m, k), (n, kb) = a.shape, b.shape
     device = a.codes.device
@@ -406,7 +414,9 @@ def rms_norm_linear(x, norm_weight, weight, residual=None, eps=1e-6, grad_dtype=
     (tokens, k) and weight (n, k), y in x's dtype.  The products run in 8 bits
     (e4m3; the output's gradient in grad_dtype); gradients pass the rounding
     straight through, and weight's comes in weight's dtype: the G of its
-    optimizer step."""
+    optimizer step.  y, and the gradient that goes back through the norm, are
+    summed as `matmul` sums x's dtype: what 16-bit results drop there also
+    reaches the gradients of x, of the residual and of norm_weight."""
     if residual is None:
         return _NormLinear.apply(x, None, norm_weight, weight, eps, grad_dtype), x
     return _NormLinear.apply(x, residual, norm_weight, weight, eps, grad_dtype)
@@ -414,5 +424,6 @@ def rms_norm_linear(x, norm_weight, weight, residual=None, eps=1e-6, grad_dtype=
 
 def scaled_linear(x, weight, grad_dtype=torch.float8_e4m3fn):
     """x weight^T for x (tokens, k) and weight (n, k) in 8-bit products, in x's
-    dtype, with the gradients of both."""
+    dtype, with the gradients of both.  The result and x's gradient are summed as
+    `matmul` sums x's dtype, weight's gradient as it sums weight's."""
     return _Linear.apply(x, weight, grad_dtype)

@@ -737,3 +737,41 @@ def test_blocked_tensor_moved_in_place(which):
     t.set_(old[:1].clone())                             # and checked there: too few rows
     with pytest.raises(ValueError):
         linear.matmul(a, b)
+
+
+@pytest.mark.parametrize("m,n", [(3, 200), (40, 500), (40, 4096), (300, 520), (1300, 2100)])
+def test_matmul_sums_that_cancel(m, n):
+    """What is left when a row's large products cancel: whole in a float32 result and its cast, within the stated bound in a 16-bit one."""
+    rng = _rng(m, n, 71)
+    # large products of one sign in the first half of k and of the other in the second, small ones between them: whole
+    # numbers whose partial sums stay below 2^24, so that fp32 sums them exactly in any order
+    x, y = np.repeat(rng.integers(1, 4, (m, 1)), 256, 1).astype(np.float64), np.repeat(rng.integers(1, 4, (n, 1)), 256, 1).astype(np.float64)
+    x[:, ::8], y[:, ::8] = 448, 448
+    x[:, 128::8] = -448
+    # and random products in cancelling pairs, on small ones of random signs
+    u, v = rng.standard_normal((m, 1024)), rng.standard_normal((n, 1024))
+    u[:, 1:896:2], v[:, 1:896:2] = -u[:, 0:896:2], v[:, 0:896:2]
+    u[:, 896:] *= 2.0 ** -7
+    for p, q, whole_numbers in ((x, y, True), (u, v, False)):
+        a, b = linear.quantize(_t(p)), linear.quantize(_t(q))
+        p, q = _held(a), _held(b)
+        k, want, size = p.shape[1], p @ q.T, np.abs(p) @ np.abs(q).T
+        assert np.linalg.norm(want) < 2.0 ** -6 * np.linalg.norm(size)
+        whole, half = linear.matmul(a, b, dtype=torch.float32), linear.matmul(a, b)
+        sums = 0.0 if whole_numbers else size * (k + 1) * ULP
+        assert (np.abs(_n(whole) - want) <= sums).all()
+        assert (np.abs(_n(whole.bfloat16()) - want) <= np.abs(want) * _half("bf16") + sums * (1 + _half("bf16"))).all()
+        most = size * ((k + 1) * ULP + 2.0 ** -10)
+        assert (np.abs(_n(half) - want) <= np.abs(want) * _half("bf16") + most * (1 + _half("bf16"))).all()
+
+
+def test_matmul_value_past_fp32():
+    """An input next to fp32's largest rounds to 2^128 in 8 bits: an infinity in a float32 result, a factor like any other in a 16-bit one."""
+    for m in (3, 70, 300):
+        x = torch.zeros(m, 256, device="cuda")
+        x[1, 7] = 3.4e38
+        for fmt in F8.values():
+            a, b = linear.quantize(x, dtype=fmt), linear.quantize(torch.full((40, 256), 2.0 ** -30, device="cuda"))
+            c = linear.matmul(a, b, dtype=torch.float32)
+            assert c[1].isposinf().all() and (c[[0, *range(2, m)]] == 0).all()
+            assert (linear.matmul(a, b)[1] == 2.0 ** 98).all()
