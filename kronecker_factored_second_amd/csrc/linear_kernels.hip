@@ -1181,6 +1181,13 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t s) {
 //  - the largest tile that still gives most of the 256 CUs one: 2048 x 5632 x
 //    2048 is 176 big tiles, 29.8 (small 32.4); 2048 x 2048 x 2048 only 64,
 //    26.9 (small 16.1); 256 x 5632 x 2048 88 small ones, 14.7 (narrow 13.2).
+//    But no 256 x 256 one for at most 128 rows or columns: at least half of
+//    it would lie past the end (us, big and small tiles): 48 x 50257 x 4096
+//    46 and 34, fp32 83 and 54; 128 x 128256 x 4096 140 and 139, fp32 212 and
+//    156; 50257 x 64 x 2048 30 and 22, fp32 51 and 33; 131072 x 128 x 2048 67
+//    and 63, fp32 113 and 84.  Up to 64 rows narrow tiles would gain at some
+//    sizes and lose at others: 17 x 50257 x 4096 32.4 (small 33.7), fp32 51
+//    (61); 48 x 128256 x 4096 139 (122), fp32 149 (139).
 //  - narrow tiles too few for the card split the sum, to about 384 workgroups,
 //    where that pays: a stage of 128 takes about 0.6 us, a split sum 3 us more
 //    and its partial sums' way at 5 TB/s.  48 x 5120 x 13824: 65.5 whole, 20.5
@@ -1193,7 +1200,7 @@ static MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k) {
     p.tile = tile, p.tm = static_cast<int>((m + bm - 1) / bm), p.tn = static_cast<int>((n + bn - 1) / bn);
     return static_cast<int64_t>(p.tm) * p.tn;
   };
-  if (tiles(3, TileBig::BM, TileBig::BN) >= 160) return p;
+  if (m > 128 && n > 128 && tiles(3, TileBig::BM, TileBig::BN) >= 160) return p;
   if (tiles(2, TileSmall::BM, TileSmall::BN) >= 160) return p;
   const int64_t t = tiles(1, TileNarrow::BM, TileNarrow::BN), blocks = (k + 127) / 128;
   int64_t s = (384 + t / 2) / t;

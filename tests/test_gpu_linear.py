@@ -775,3 +775,12 @@ def test_matmul_value_past_fp32():
             c = linear.matmul(a, b, dtype=torch.float32)
             assert c[1].isposinf().all() and (c[[0, *range(2, m)]] == 0).all()
             assert (linear.matmul(a, b)[1] == 2.0 ** 98).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(17, 41100, 260), (100, 41000, 130), (128, 41217, 129), (129, 41000, 130), (20500, 3, 300), (41000, 1, 130),
+                                   (41100, 128, 257), (41000, 129, 130)])
+def test_matmul_few_rows_through_many_columns(m, n, k, kind):
+    """Vocabulary-wide products of a decode batch, and many tokens into few columns, on both sides of where the tile changes."""
+    a, b = _operands(m, n, k, key=13)
+    _check_product(linear.matmul(a, b, dtype=FLOATS[kind]), a, b, kind)
