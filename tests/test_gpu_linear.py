@@ -784,3 +784,99 @@ def test_matmul_few_rows_through_many_columns(m, n, k, kind):
     """Vocabulary-wide products of a decode batch, and many tokens into few columns, on both sides of where the tile changes."""
     a, b = _operands(m, n, k, key=13)
     _check_product(linear.matmul(a, b, dtype=FLOATS[kind]), a, b, kind)
+
+
+def test_side_stream_in_order():
+    """Every operator, forward and backward, runs on the current stream: behind a side stream's own queued work, whose results it reads.
+    Launched on another stream it would read the values from before."""
+    rng = _rng(100)
+    m, k, n = 300, 700, 260
+
+    def inputs(key):
+        g = _rng(key)
+        return [_t(_values(g, m, k), "bf16"), _t(_values(g, m, k), "bf16"), _t(1 + 0.2 * g.standard_normal(k)), _t(0.05 * g.standard_normal((n, k))),
+                _t(g.standard_normal((m, n)), "bf16")]
+
+    def calls(x, r, w, W, dy):
+        q, h, rstd = linear.rms_norm(x, w, residual=r)
+        a, at = linear.quantize_both(W)
+        out = linear.matmul(q, a)
+        dq, dt = linear.quantize_both(dy)
+        single = (q.codes.view(torch.uint8), h, rstd, out, linear.matmul(dt, linear.quantize(h, transpose=True, row_factor=rstd, col_factor=w), dtype=torch.float32),
+                  *linear.rms_norm_backward(linear.matmul(dq, at), h, rstd, w, dh=h))
+        leaves = [t.detach().requires_grad_() for t in (x, r, w, W)]
+        y, s = linear.rms_norm_linear(leaves[0], leaves[2], leaves[3], residual=leaves[1])
+        z = linear.scaled_linear(s, leaves[3])
+        return (*single, y.detach(), z.detach(), *torch.autograd.grad((y, s, z), leaves, (dy, h, dy)))
+
+    before, after = inputs(1), inputs(2)
+    old, want = calls(*before), calls(*after)
+    assert not any(torch.equal(a, b) for a, b in zip(old, want))        # the values from before would be told apart
+    heavy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(20):                         # some milliseconds ahead of the inputs' new values
+            heavy = torch.mm(heavy, heavy) * 1e-2
+        for t, v in zip(before, after):
+            t.copy_(v)
+        got = calls(*before)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("m,k", [((1 << 20) + 101, 2048), (54000, 40000)])
+def test_more_elements_than_32_bits_count(m, k):
+    """More than 2^31 elements in each tensor: the last rows come as they do from a matrix of their own."""
+    def stream(seed):
+        return torch.randn(m, k, dtype=torch.bfloat16, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed))
+    x, r = stream(1), stream(2)
+    assert x.numel() > 1 << 31
+    w = _t(1 + 0.2 * _rng(14).standard_normal(k))
+    start = (m - 64) // 128 * 128                   # a block of the transposed form begins there
+    tail = slice(start, m)
+
+    def tails(q):
+        return q.codes.view(torch.uint8)[tail], q.scales.view(torch.uint8)[:, tail]
+
+    q, h, rstd = linear.rms_norm(x, w, residual=r)
+    small = linear.rms_norm(x[tail], w, residual=r[tail])
+    assert torch.equal(h[tail], small.h) and torch.equal(rstd[tail], small.rstd)
+    assert all(torch.equal(a, b) for a, b in zip(tails(q), _bits(small.q)))
+    # a product that reads the last rows of such a matrix
+    b = linear.quantize(_t(_rng(15).standard_normal((20, k))))
+    _check_product(linear.matmul(q, b)[tail], small.q, b, "bf16")
+    del q
+    # gradients, r as dy and x as what reaches h
+    dx, dw = linear.rms_norm_backward(r, h, rstd, w, dh=x)
+    part, _ = linear.rms_norm_backward(r[tail], h[tail], rstd[tail], w, dh=x[tail])
+    assert torch.equal(dx[tail], part)
+    want, size = torch.zeros(k, dtype=torch.float64, device="cuda"), torch.zeros(k, dtype=torch.float64, device="cuda")
+    for i in range(0, m, 16384):
+        p = r[i:i + 16384].double() * (h[i:i + 16384].double() * rstd[i:i + 16384].double()[:, None])
+        want += p.sum(0)
+        size += p.abs().sum(0)
+    # a workgroup sums every 256th row at the most in fp32, the workgroups' sums are added in fp64
+    assert ((dw.double() - want).abs() <= want.abs() * 2.0 ** -24 + size * (-(-m // 256) + 8) * ULP).all()
+    del dx, r, rstd
+    q, t = linear.quantize_both(h)
+    one, other = linear.quantize_both(h[tail])
+    assert all(torch.equal(a, b) for a, b in zip(tails(q), _bits(one)))
+    assert torch.equal(t.codes.view(torch.uint8)[:, start:m], other.codes.view(torch.uint8)[:, :m - start])
+    assert torch.equal(t.scales.view(torch.uint8)[start // 128:, :k], other.scales.view(torch.uint8)[:, :k])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_matmul_result_of_more_elements_than_32_bits_count(kind):
+    """Whole numbers, which every order of summation adds exactly: the last rows as from operands of their own."""
+    m, n, k = 65700, 32800, 128
+    rng = _rng(16)
+    x, y = _t(rng.integers(-4, 5, (m, k))), _t(rng.integers(-4, 5, (n, k)))
+    a, b = linear.quantize(x), linear.quantize(y)
+    c = linear.matmul(a, b, dtype=FLOATS[kind])
+    assert c.numel() > 1 << 31
+    assert torch.equal(c[-300:], linear.matmul(linear.quantize(x[-300:]), b, dtype=FLOATS[kind]))
+    assert torch.equal(c[:300], (x[:300] @ y.T).to(FLOATS[kind]))
+    assert torch.equal(c[-300:], (x[-300:] @ y.T).to(FLOATS[kind]))
+    once = x[-300:] @ y.T
+    assert torch.equal(linear.matmul(a, b, out=c, accumulate=True)[-300:], (once.to(c.dtype).float() + once).to(c.dtype))
