@@ -880,3 +880,39 @@ def test_matmul_result_of_more_elements_than_32_bits_count(kind):
     assert torch.equal(c[-300:], (x[-300:] @ y.T).to(FLOATS[kind]))
     once = x[-300:] @ y.T
     assert torch.equal(linear.matmul(a, b, out=c, accumulate=True)[-300:], (once.to(c.dtype).float() + once).to(c.dtype))
+
+
+def test_layer_pass_in_a_graph():
+    """A layer's forward and backward captured once and replayed on new inputs, with eager passes over other leaves between the replays."""
+    m, k, n = 300, 640, 520
+
+    def inputs(i):
+        g = _rng(i, 113)
+        return [_t(_values(g, m, k), "bf16"), _t(_values(g, m, k), "bf16"), _t(1 + 0.1 * g.standard_normal(k)), _t(0.05 * g.standard_normal((n, k))), _t(g.standard_normal((m, n)), "bf16")]
+
+    def layer(x, r, w, W, dy):
+        y, h = linear.rms_norm_linear(x, w, W, residual=r)
+        z = linear.scaled_linear(h, W)
+        return (y.detach(), h.detach(), z.detach(), *torch.autograd.grad((y, z, h), (x, r, w, W), (dy, dy, x.detach())))
+
+    held = inputs(0)
+    leaves = [t.requires_grad_() for t in held[:4]] + held[4:]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(*leaves)                              # its graph is gone before the capture begins
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = layer(*leaves)
+    for i in range(4):
+        new = inputs(i)
+        with torch.no_grad():
+            for t, v in zip(held, new):
+                t.copy_(v)
+        want = layer(*[t.requires_grad_() for t in new[:4]], new[4])
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
