@@ -391,8 +391,10 @@ __global__ __launch_bounds__(kThreads<THR>) void rms_norm_kernel(NormArgs a) {
 constexpr int kGradBlocks = 1024;   // most workgroups of a launch, each with one row of partial sums of dweight
 
 // The same layout.  A thread meets the same columns in every row, so dweight's
-// sums stay in its registers (fp32, at most rows / 2 of them); a workgroup
-// leaves one row of partial sums, which norm_dw_kernel adds in fp64.
+// sums stay in its registers, in fp32: ceil(rows / workgroups) terms one after
+// the other, a quarter of that where a wave takes a row, so 16 in a batch of
+// 16384 x 2048 and 1024 in 2^20 rows of it.  A workgroup leaves one row of
+// partial sums, which norm_dw_kernel adds in fp64.
 // Bound by memory: 16384 x 2048 bf16 with dh moves 268 MB in 57 us (4.7 TB/s,
 // the join's 5 us included); with the sums in memory it took 172 us, with dy and
 // h held as floats 99.  fp32 777 x 5121 takes 18 us for 48 MB: its partial rows,
@@ -614,10 +616,12 @@ __device__ __forceinline__ void put8(T* c, float (&v)[8], int n, int accumulate)
 // Codes and scales come by direct-to-LDS copies, two stages of 128 of k deep, so
 // a stage has the whole of the one before to arrive in.
 // Bound by the matrix cores at the clock they can hold: 8192 x 8192 x 8192 runs
-// at 2.7 PFLOP/s (16-bit results; 70 % of the cycles issue products, at 1.7 GHz
-// of 2.4), 11008 x 4096 x 16384 in fp32 at 1.35-1.4 (77 %, 1.8 GHz).  Short k
-// pays each tile's start and its output's burst: 8191 x 5632 x 2048 runs at 2.1,
-// 176 tiles (5632 x 2048 x 8192 in fp32) leave 80 of 256 CUs idle, 1.2.
+// at 2.7 PFLOP/s (16-bit results; 72 % of a busy CU's cycles issue products, at
+// 1.85 GHz of 2.4), 11008 x 4096 x 16384 in fp32 at 1.35-1.4 (76 %, 1.85 GHz).
+// Short k pays each tile's start and its output's burst: 8191 x 5632 x 2048 runs
+// at 2.1 (54 %), 176 tiles (5632 x 2048 x 8192 in fp32) leave 80 of 256 CUs
+// idle, 1.0-1.15.  LDS bank conflicts are counted in one place only: 1024 cycles a
+// big tile, at any k, where its 16-bit results are staged on their way out.
 // A loop over tiles that let a tile's stores drain behind the next one's
 // products measured the same and cost the registers of the loop.
 template <int WM_, int WN_, int GI_, int GJ_>
@@ -958,7 +962,7 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(MatmulArgs a, int spli
 // with the launch in it.
 // Few rows of a (16 TM of them a workgroup): c's columns in groups of 16 TN a workgroup,
 // whose waves split the summed axis in turn and add up through LDS.  Every code
-// of b is read once and straight into registers, eight blocks of 128 ahead.
+// of b is read once and straight into registers, U blocks of 128 a wave at a time.
 constexpr int kFewWaves = 8;
 template <int TM, int TN, int FA, int FB, bool F32>
 __global__ __launch_bounds__(kFewWaves * 64) void matmul_few_kernel(MatmulArgs a) {
