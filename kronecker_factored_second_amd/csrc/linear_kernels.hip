@@ -550,11 +550,14 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* part, int n_
 // 2^-13 of it before the fp32 addition (measured on this card, the same in the
 // unscaled instruction): about 1.6e-5 of a result in norm.  That is far below
 // a 16-bit result's own rounding (1.7e-3 in bf16, 2e-4 in fp16), so 16-bit
-// results take it; fp32 results, which go into the optimizer's factors, would
-// lose nine bits.  They convert codes times scale to bf16, which holds every
-// such value exactly (4 significant bits; a value below 2^-126, subnormal in
-// fp32, may count as zero), and take the bf16 instruction, whose sums round as
-// fp32's.
+// results take it, at the price of elements whose large products cancel: there
+// up to 8 2^-13 of the sizes' sum is lost (448^2 and -448^2, each in a group of
+// eight with seven products of 1, leave 0 of the 14).  A caller to whom that
+// counts asks for fp32 results.  Those, which also go into the optimizer's
+// factors, would lose nine bits.  They convert codes times scale to bf16, which
+// holds every such value exactly (4 significant bits; a value below 2^-126,
+// subnormal in fp32, may count as zero, and 2^128 is an infinity), and take the
+// bf16 instruction, whose sums round as fp32's.
 
 // cbsz / blgp of the f8f6f4 instructions: 0 e4m3, 1 e5m2 (the okls_code values)
 

@@ -256,7 +256,8 @@ def quantize_both(x, dtype=torch.float8_e4m3fn, row_factor=None, col_factor=None
 
 def matmul(a: Blocked, b: Blocked, dtype=torch.bfloat16, out=None, accumulate=False):
     """a b^T for a (m, k) and b (n, k) in 8 bits: (m, n) of `dtype`, or into
-    `out` (of its own dtype); accumulate=True adds to what `out` holds.
+    `out` (of its own dtype); accumulate=True adds to what `out` holds.  Autograd
+    sees the write; an `out` that requires a gradient is refused while it records.
 
     A float32 result sums the exact products in fp32.  A 16-bit result is summed
     in fp32 and rounded once, but from each eight products the 8-bit matrix
@@ -424,6 +425,7 @@ def rms_norm_linear(x, norm_weight, weight, residual=None, eps=1e-6, grad_dtype=
 
 def scaled_linear(x, weight, grad_dtype=torch.float8_e4m3fn):
     """x weight^T for x (tokens, k) and weight (n, k) in 8-bit products, in x's
-    dtype, with the gradients of both.  The result and x's gradient are summed as
+    dtype, with the gradients of both.  weight is brought to 8 bits in every call;
+    to serve, keep `quantize(weight)` and call `matmul`.  The result and x's gradient are summed as
     `matmul` sums x's dtype, weight's gradient as it sums weight's."""
     return _Linear.apply(x, weight, grad_dtype)

@@ -916,3 +916,23 @@ def test_layer_pass_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("m", [1, 5, 70, 400])
+def test_forward_without_gradients(m):
+    """Serving: the operators under no_grad and inference_mode, and the single calls on a weight quantised once, give a training forward's bits."""
+    rng = _rng(m, 114)
+    x, r, nw = _t(_values(rng, m, 300), "bf16"), _t(_values(rng, m, 300), "bf16"), _t(1 + 0.2 * rng.standard_normal(300)).requires_grad_()
+    W = _t(0.05 * rng.standard_normal((500, 300))).requires_grad_()
+    y, h = linear.rms_norm_linear(x, nw, W, residual=r)
+    z = linear.scaled_linear(h, W)
+    assert y.requires_grad and z.requires_grad
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            a, s = linear.rms_norm_linear(x, nw, W, residual=r)
+            b = linear.scaled_linear(s, W)
+            assert not a.requires_grad and not b.requires_grad
+            kept = linear.quantize(W)
+            q, t, _ = linear.rms_norm(x, nw, residual=r)
+            for got, want in ((a, y), (s, h), (b, z), (t, h), (linear.matmul(q, kept), y), (linear.matmul(linear.quantize(t), kept), z)):
+                assert torch.equal(got, want)
