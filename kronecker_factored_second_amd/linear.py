@@ -425,7 +425,8 @@ def rms_norm_linear(x, norm_weight, weight, residual=None, eps=1e-6, grad_dtype=
 
 def scaled_linear(x, weight, grad_dtype=torch.float8_e4m3fn):
     """x weight^T for x (tokens, k) and weight (n, k) in 8-bit products, in x's
-    dtype, with the gradients of both.  weight is brought to 8 bits in every call;
-    to serve, keep `quantize(weight)` and call `matmul`.  The result and x's gradient are summed as
-    `matmul` sums x's dtype, weight's gradient as it sums weight's."""
+    dtype, with the gradients of both.  The result and x's gradient are summed as
+    `matmul` sums x's dtype, weight's gradient as it sums weight's.  weight is
+    brought to 8 bits in every call; to serve, keep `quantize(weight)` and call
+    `matmul`."""
     return _Linear.apply(x, weight, grad_dtype)
