@@ -355,7 +355,9 @@ def prepare(case, seed):
         s["x"].requires_grad_()
     elif op == "product":
         s["a"] = _quantised(_gathered(_stream(g, t, c["k"], 0.5), s["plan"][1], c["each"]), c["format"])
-        s["b"] = _quantised(0.02 * torch.randn(e * c["n"], c["k"], generator=g, device="cuda"), "e4m3")
+        # each expert's rows begin at a multiple of 16
+        stack = torch.nn.functional.pad(0.02 * torch.randn(e, c["n"], c["k"], generator=g, device="cuda"), (0, 0, 0, -c["n"] % 16))
+        s["b"] = _quantised(stack.reshape(-1, c["k"]), "e4m3")
     elif op == "weight_grad":
         s["a"] = _quantised(_gathered(_stream(g, t * c["each"], c["n"], 1e-2), s["plan"][1], 1).T, c["format"])
         s["b"] = _quantised(_gathered(_stream(g, t, c["k"], 0.5), s["plan"][1], c["each"]).T, "e4m3")
@@ -400,7 +402,7 @@ def _run_own(s):
         xs, y = experts.gather(s["x"], plan), experts.combine(s["ys"], s["weights"], plan)
         return list(torch.autograd.grad((xs, y), (s["x"], s["ys"], s["weights"]), (s["dxs"], s["dy"])))
     if op == "product":
-        a, b = linear.Blocked(*s["a"], (rows, c["k"])), linear.Blocked(*s["b"], (e * c["n"], c["k"]))
+        a, b = linear.Blocked(*s["a"], (rows, c["k"])), experts.Stack(*s["b"], (e, c["n"], c["k"]))
         return experts.matmul(a, b, plan, dtype=FLOATS[c["type"]])
     a, b = linear.Blocked(*s["a"], (c["n"], rows)), linear.Blocked(*s["b"], (c["k"], rows))
     return experts.weight_grad(a, b, plan, dtype=FLOATS[c["type"]])
@@ -430,7 +432,7 @@ def _run_plain(s):
         xs, y = _gathered(s["x"], s["plan"][1], c["each"]), _combined(s["ys"], s["plan"][0], s["weights"])
         return [_combined(s["dxs"], s["plan"][0], None), *_combine_grads(s["dy"], s["ys"], *s["plan"][:2], s["weights"])]
     if op == "product":
-        return _products(_values(s["a"], rows, k), _values(s["b"], e * n, k).reshape(e, n, k), *s["spans"], FLOATS[c["type"]])
+        return _products(_values(s["a"], rows, k), _values(s["b"], e * _up(n, 16), k).reshape(e, -1, k)[:, :n], *s["spans"], FLOATS[c["type"]])
     if op == "weight_grad":
         return _weight_products(_values(s["a"], n, rows), _values(s["b"], k, rows), *s["spans"])
     plan = _plan(s["choice"], c)
@@ -597,10 +599,11 @@ def exact(case, seed):
         return pair[0][:, :cols].double() * pair[1][:, :r].double().T.repeat_interleave(128, 1)[:, :cols]
 
     if op == "product":
-        a, b = held(s["a"], rows, k), held(s["b"], e * n, k)
+        step = s["b"][0].shape[0] // e
+        a, b = held(s["a"], rows, k), held(s["b"], e * step, k)
         out = torch.zeros(rows, n, dtype=torch.float64, device="cuda")
         for q, m, at in lay:
-            out[at: at + len(m)] = a[at: at + len(m)].mm(b[q * n: (q + 1) * n].T)
+            out[at: at + len(m)] = a[at: at + len(m)].mm(b[q * step: q * step + n].T)
         return out
     if op == "weight_grad":
         a, b = held(s["a"], n, rows), held(s["b"], k, rows)
