@@ -359,8 +359,8 @@ def prepare(case, seed):
         stack = torch.nn.functional.pad(0.02 * torch.randn(e, c["n"], c["k"], generator=g, device="cuda"), (0, 0, 0, -c["n"] % 16))
         s["b"] = _quantised(stack.reshape(-1, c["k"]), "e4m3")
     elif op == "weight_grad":
-        s["a"] = _quantised(_gathered(_stream(g, t * c["each"], c["n"], 1e-2), s["plan"][1], 1).T, c["format"])
-        s["b"] = _quantised(_gathered(_stream(g, t, c["k"], 0.5), s["plan"][1], c["each"]).T, "e4m3")
+        s["a"] = _quantised(_gathered(_stream(g, t * c["each"], c["n"], 1e-2), s["plan"][1], 1).T.contiguous(), c["format"])
+        s["b"] = _quantised(_gathered(_stream(g, t, c["k"], 0.5), s["plan"][1], c["each"]).T.contiguous(), "e4m3")
     elif op == "layer":
         s["x"] = _stream(g, t, c["k"], 0.5).bfloat16().requires_grad_()
         s["weights"] = weights.bfloat16().requires_grad_()
