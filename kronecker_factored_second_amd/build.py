@@ -4,7 +4,8 @@ import subprocess
 import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-SOURCES = ["csrc/okls_api.cpp", "csrc/okls_kernels.hip", "csrc/linear_api.cpp", "csrc/linear_kernels.hip"]
+SOURCES = ["csrc/okls_api.cpp", "csrc/okls_kernels.hip", "csrc/linear_api.cpp", "csrc/linear_kernels.hip",
+           "csrc/optim_api.cpp", "csrc/optim_kernels.hip", "csrc/experts_api.cpp", "csrc/experts_kernels.hip"]
 OUT = os.path.join(HERE, "libokls.so")
 
 

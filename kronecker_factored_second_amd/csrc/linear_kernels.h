@@ -19,6 +19,13 @@ struct QuantArgs {
   const void* col_factor;
   int32_t x_dtype, col_dtype;
   Blocked along_cols, along_rows;
+  // a stack of matrices, `stride` elements apart in x; the outputs' are multiples of 16 rows apart
+  int32_t batch;
+  int64_t stride;
+  // rows in the sorted order of experts: row r holds choice pairs[r], -1 none; x's row
+  // pairs[r] / each, or r itself where each is 0
+  const int32_t* pairs;
+  int32_t each, n_pairs;
 };
 
 struct MatmulArgs {
