@@ -36,7 +36,7 @@ struct NormTensor {
   int32_t dtype;
 };
 constexpr int kNormTensors = 128;
-constexpr int kNormChunk = 8192;   // elements a workgroup
+constexpr int kNormChunk = 32768;  // elements a workgroup
 
 struct GradNormArgs {
   NormTensor tensor[kNormTensors];

@@ -89,25 +89,14 @@ __device__ __forceinline__ uint2 codes_at(const uint8_t* codes, int n) {
   return uint2{w[0], w[1]};
 }
 
-// 2048 elements of one tensor a workgroup, eight a thread: a block of 128 is 16
-// neighbouring lanes.
-template <bool EIGHT>
-__global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
-  const int at = __builtin_amdgcn_readfirstlane(tensor_of(a.tensor, a.count, blockIdx.x));
-  const AdamTensor& t = a.tensor[at];
-  const int64_t i = static_cast<int64_t>(blockIdx.x - t.first) * kAdamChunk + threadIdx.x * 8;
-  const int n = clamp8(t.n - i);
-  float factor = 1.0f;
-  if (a.norm != nullptr) {
-    const float norm = *a.norm;
-    if (!(fabsf(norm) < __builtin_inff())) return;
-    const double f = a.max_norm / (static_cast<double>(norm) + 1e-6);
-    factor = static_cast<float>(f < 1.0 ? f : 1.0);
-  }
+// One thread's eight elements.  The gradient's type is known here, so that every
+// load is on its way before the first is used.
+template <typename G, bool EIGHT>
+__device__ __forceinline__ void adamw8(const AdamArgs& a, const AdamTensor& t, int64_t i, int n, float factor) {
   float p[8], g[8], m[8], v[8], s[8];
-  load8(p, t.p + i, n);
-  load8_any(g, t.g, i, n, a.dtype[at]);
   const int64_t blocks = (t.n + 127) >> 7, block = i >> 7;
+  load8(p, t.p + i, n);
+  const Raw8<G> raw = raw8(static_cast<const G*>(t.g) + i, n);
   if constexpr (EIGHT) {
     const float scale_m = n > 0 ? scale_value(t.scales[block]) : 0.0f, scale_s = n > 0 ? scale_value(t.scales[blocks + block]) : 0.0f;
     decode8(m, codes_at(static_cast<const uint8_t*>(t.m) + i, n));
@@ -122,6 +111,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
     load8(m, static_cast<const float*>(t.m) + i, n);
     load8(v, static_cast<const float*>(t.v) + i, n);
   }
+  widen8(g, raw);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (a.norm != nullptr) g[j] = g[j] * factor;
@@ -151,6 +141,27 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
   }
 }
 
+// 2048 elements of one tensor a workgroup, eight a thread: a block of 128 is 16
+// neighbouring lanes.
+template <bool EIGHT>
+__global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
+  const int at = __builtin_amdgcn_readfirstlane(tensor_of(a.tensor, a.count, blockIdx.x));
+  const AdamTensor& t = a.tensor[at];
+  const int64_t i = static_cast<int64_t>(blockIdx.x - t.first) * kAdamChunk + threadIdx.x * 8;
+  const int n = clamp8(t.n - i);
+  float factor = 1.0f;
+  if (a.norm != nullptr) {
+    const float norm = *a.norm;
+    if (!(fabsf(norm) < __builtin_inff())) return;
+    const double f = a.max_norm / (static_cast<double>(norm) + 1e-6);
+    factor = static_cast<float>(f < 1.0 ? f : 1.0);
+  }
+  const int dtype = a.dtype[at];
+  if (dtype == OKLS_F32) adamw8<float, EIGHT>(a, t, i, n, factor);
+  else if (dtype == OKLS_BF16) adamw8<bf16_t, EIGHT>(a, t, i, n, factor);
+  else adamw8<half_t, EIGHT>(a, t, i, n, factor);
+}
+
 template <int THREADS>
 __device__ __forceinline__ double block_sum(double v) {
   __shared__ double sh[THREADS / 64];
@@ -164,20 +175,35 @@ __device__ __forceinline__ double block_sum(double v) {
   return v;
 }
 
+// a thread's share of a chunk's squares: its type known, so that four loads are on their way at once
+template <typename G>
+__device__ __forceinline__ double squares(const NormTensor& t, int64_t first) {
+  double sum = 0.0;
+  for (int64_t i = first + threadIdx.x * 8; i < t.n && i < first + kNormChunk; i += 4 * 2048) {
+    Raw8<G> g[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) g[q] = raw8(static_cast<const G*>(t.g) + i + q * 2048, clamp8(t.n - i - q * 2048));
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double v = element(g[q], j);
+        sum = fma(v, v, sum);
+      }
+  }
+  return sum;
+}
+
 __global__ __launch_bounds__(256) void grad_norm_kernel(GradNormArgs a) {
   const int half = a.count < 64 ? a.count : 64;
   int at = tensor_of(a.tensor, half, blockIdx.x);
   if (a.count > 64) at += tensor_of(a.tensor + 64, a.count - 64, blockIdx.x) + 1;
   const NormTensor& t = a.tensor[__builtin_amdgcn_readfirstlane(at)];
-  const int64_t i = static_cast<int64_t>(blockIdx.x - t.first) * kNormChunk + threadIdx.x * 8;
-  double sum = 0.0;
-  float g[4][8];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) load8_any(g[q], t.g, i + q * 2048, clamp8(t.n - i - q * 2048), t.dtype);
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fma(static_cast<double>(g[q][j]), static_cast<double>(g[q][j]), sum);
+  const int64_t first = static_cast<int64_t>(blockIdx.x - t.first) * kNormChunk;
+  double sum;
+  if (t.dtype == OKLS_F32) sum = squares<float>(t, first);
+  else if (t.dtype == OKLS_BF16) sum = squares<bf16_t>(t, first);
+  else sum = squares<half_t>(t, first);
   sum = block_sum<256>(sum);
   if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
 }

@@ -371,14 +371,18 @@ class _Linear(torch.autograd.Function):
 
 def gather(x, order: Plan):
     """Tokens' rows x (tokens, k) in the sorted order: (order.capacity, k), zeros in rows without a choice."""
-    return _Gather.apply(x, order)
+    if x.requires_grad and torch.is_grad_enabled():
+        return _Gather.apply(x, order)
+    return _gather(x, order)
 
 
 def combine(y, weights, order: Plan):
     """Each token's sum over its choices of weights (tokens, each) times their rows of
     y (order.capacity, k), in fp32, rounded once: (tokens, k) in y's dtype.  Dropped choices add
     nothing, and what y holds in rows without a choice is not read.  weights=None: ones."""
-    return _Combine.apply(y, weights, order)
+    if torch.is_grad_enabled() and (y.requires_grad or (weights is not None and weights.requires_grad)):
+        return _Combine.apply(y, weights, order)
+    return _combine(y, None if weights is None else _weights(weights, order), order)
 
 
 def linear(x, weight, order: Plan, grad_dtype=torch.float8_e4m3fn):

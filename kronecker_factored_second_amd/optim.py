@@ -85,16 +85,15 @@ def grad_norm(grads) -> torch.Tensor:
     grads = [g if g.is_contiguous() else g.contiguous() for g in grads]
     if not grads:
         raise ValueError("no gradients")
-    device, dtypes = grads[0].device, linear.DTYPES
-    table = (GradientStruct * len(grads))()
+    device, index, dtypes, flat = grads[0].device, grads[0].get_device(), linear.DTYPES, []
     for i, g in enumerate(grads):
         dtype = dtypes.get(g.dtype)
         if dtype is None:
             raise ValueError(f"gradient {i} must be float32, bfloat16 or float16, got {g.dtype}")
-        if g.device != device or not g.is_cuda:
+        if g.get_device() != index or index < 0:
             raise ValueError(f"gradient {i} is on {g.device}, the first on {device}: all must be on one GPU")
-        e = table[i]
-        e.data, e.n, e.dtype = g.data_ptr(), g.numel(), dtype
+        flat += (g.data_ptr(), g.numel(), dtype)
+    table = (ctypes.c_uint64 * len(flat))(*flat)        # of GradientStruct
     need = (_lib or load()).okls_grad_norm_workspace_size(len(grads), table)
     ws = torch.empty(need, dtype=torch.uint8, device=device)
     norm = torch.empty((), dtype=torch.float32, device=device)
@@ -120,41 +119,37 @@ def adamw(params, grads, moments, t, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, 
         raise ValueError("no parameters")
     if len(grads) != len(params) or len(moments) != len(params):
         raise ValueError(f"{len(grads)} gradients and {len(moments)} moments for {len(params)} parameters")
-    device, dtypes, float32 = params[0].device, linear.DTYPES, torch.float32
-    if not params[0].is_cuda:
+    device, index, dtypes, float32 = params[0].device, params[0].get_device(), linear.DTYPES, torch.float32
+    if index < 0:
         raise ValueError(f"parameter 0 must be on a GPU, got {device}")
     eight = moments[0][2] is not None
     held = torch.float8_e4m3fn if eight else float32
-    table, kept, seen = (TensorStruct * len(params))(), [], set()
+    flat, kept = [], []
     for i, (p, g, (m, v, scales)) in enumerate(zip(params, grads, moments)):
-        shape, n = p.shape, p.numel()
-        if p.dtype != float32 or p.device != device or not p.is_contiguous():
+        n = p.numel()
+        if p.dtype is not float32 or p.get_device() != index or not p.is_contiguous():
             raise ValueError(f"parameter {i} must be a contiguous float32 tensor on {device}, got {p.dtype} on {p.device}")
         dtype = None if g is None else dtypes.get(g.dtype)
         if dtype is None:
             raise ValueError(f"gradient {i} must be float32, bfloat16 or float16, got {'none' if g is None else g.dtype}")
-        if g.shape != shape or g.device != device:
-            raise ValueError(f"gradient {i} is {tuple(g.shape)} on {g.device}, parameter {tuple(shape)} on {device}")
+        if not g.is_same_size(p) or g.get_device() != index:
+            raise ValueError(f"gradient {i} is {tuple(g.shape)} on {g.device}, parameter {tuple(p.shape)} on {device}")
         if not g.is_contiguous():
             g = g.contiguous()
             kept.append(g)
-        if (m.dtype != held or v.dtype != held or m.numel() != n or v.numel() != n or m.device != device or v.device != device
-                or not m.is_contiguous() or not v.is_contiguous()):
+        if (m.dtype is not held or v.dtype is not held or m.numel() != n or v.numel() != n or m.get_device() != index
+                or v.get_device() != index or not m.is_contiguous() or not v.is_contiguous()):
             raise ValueError(f"moments {i} must be contiguous {held} tensors of {n} elements on {device}, got "
                              f"{tuple(m.shape)} {m.dtype} on {m.device} and {tuple(v.shape)} {v.dtype} on {v.device}")
-        if (scales is not None) != eight or (eight and (scales.dtype != torch.float8_e8m0fnu or tuple(scales.shape) != (2, -(-n // 128))
-                                                        or scales.device != device or not scales.is_contiguous())):
-            raise ValueError(f"scales {i} must be {f'float8_e8m0fnu {(2, -(-n // 128))} on {device}, contiguous' if eight else 'None'}, "
+        if (scales is not None) != eight or (eight and (scales.dtype is not torch.float8_e8m0fnu or scales.shape != (2, -(-n // 128))
+                                                        or scales.get_device() != index or not scales.is_contiguous())):
+            raise ValueError(f"scales {i} must be {f'contiguous float8_e8m0fnu {(2, -(-n // 128))} on {device}' if eight else 'None'}, "
                              f"got {None if scales is None else (scales.dtype, tuple(scales.shape), scales.device)}")
-        at = p.data_ptr()
-        if n:
-            if at in seen:
-                raise ValueError(f"parameter {i} is in the list twice")
-            seen.add(at)
-        e = table[i]
-        e.p, e.g, e.m, e.v, e.n, e.g_dtype = at, g.data_ptr(), m.data_ptr(), v.data_ptr(), n, dtype
-        if eight:
-            e.scales = scales.data_ptr()
+        flat += (p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), scales.data_ptr() if eight else 0, n, dtype)
+    table = (ctypes.c_uint64 * len(flat))(*flat)        # of TensorStruct
+    places = [at for at, n in zip(flat[::7], flat[5::7]) if n]
+    if len(set(places)) != len(places):
+        raise ValueError("a parameter is in the list twice")
     if norm is not None:
         if norm.dtype != float32 or norm.numel() != 1 or norm.device != device:
             raise ValueError(f"norm must be one float32 on {device}, got {tuple(norm.shape)} {norm.dtype} on {norm.device}")
