@@ -157,7 +157,8 @@ def adamw(params, grads, moments, t, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, 
             raise ValueError("norm needs max_norm")
     config = ConfigStruct(lr, beta1, beta2, eps, weight_decay, max_norm if norm is not None else 0.0, 8 if eight else 32)
     _on(device, "okls_adamw", config, t, len(params), table, None if norm is None else norm.data_ptr())
-    linear._written(params)     # a graph that kept one has to know, as of torch's own writes
+    # a graph that kept one has to know, as of torch's own writes
+    linear._written([p for p in params if not p.is_inference()])
 
 
 def new_moments(p, moments="fp32") -> Moments:
