@@ -221,6 +221,16 @@ __device__ __forceinline__ float weights_of(const RowsArgs& a, int64_t token, in
 __device__ __forceinline__ int at_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 __device__ __forceinline__ float at_lane(float v, int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); }
 
+// raw8 of what is not read again: past the caches
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8_once(const T* p, int n) {
+  if (n < 8) return raw8(p, n);
+  Raw8<T> r;
+  if constexpr (sizeof(T) == 4) r.a = __builtin_nontemporal_load(reinterpret_cast<const floatx4_any*>(p)), r.b = __builtin_nontemporal_load(reinterpret_cast<const floatx4_any*>(p) + 1);
+  else r.v = __builtin_nontemporal_load(reinterpret_cast<const u16x8_any*>(p));
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ void put_raw8(T* p, const Raw8<T>& r, int n) {
   if (n >= 8) {
@@ -252,18 +262,21 @@ __device__ __forceinline__ void zero_rows(const ExpertPlan& p, T* out, int64_t l
   for (int64_t r = static_cast<int64_t>(max(p.offsets[p.n_experts], 0)) + wave; r < p.capacity; r += waves) clear(r);
 }
 
+// What a lane holds for others (a row's number, a weight) is read from it where all
+// lanes are active: loops run over the wave's columns, and lanes past the end hold 0 of them.
+//
 // How a launch shares out tokens and columns: `waves` of a workgroup's four stand
 // side by side on one token's parts of 512 columns, 4 / waves tokens a workgroup;
 // gridDim.y workgroups along a row where there are few tokens.
 struct Place {
   int64_t token, step;        // the wave's first token, and from one to its next
-  int64_t column, stride;     // this lane's first column, and from one to its next
+  int64_t column, stride;     // the wave's first 512 columns, and from them to its next
 };
 __device__ __forceinline__ Place place(int block, int blocks, int waves) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), each = 4 / waves;
   const int part = blockIdx.y * waves + wave % waves;
   return {static_cast<int64_t>(block) * each + wave / waves, static_cast<int64_t>(blocks) * each,
-          (part * 64 + (threadIdx.x & 63)) * 8, static_cast<int64_t>(gridDim.y) * waves * 512};
+          part * int64_t(512), static_cast<int64_t>(gridDim.y) * waves * 512};
 }
 
 template <typename T>
@@ -279,7 +292,8 @@ __global__ __launch_bounds__(256) void gather_kernel(RowsArgs a, int waves) {
   for (int64_t t = at.token; t < p.tokens; t += at.step)
     for (int k0 = 0; k0 < p.each; k0 += 64) {
       const int row = rows_of(p, t, k0), ks = min(p.each - k0, 64);
-      for (int64_t c = at.column; c < a.cols; c += at.stride) {
+      for (int64_t c0 = at.column; c0 < a.cols; c0 += at.stride) {
+        const int64_t c = c0 + (threadIdx.x & 63) * 8;
         const int n = clamp8(a.cols - c);
         const Raw8<T> v = raw8(x + t * a.ldx + c, n);
         for (int k = 0; k < ks; ++k) {
@@ -300,7 +314,8 @@ __global__ __launch_bounds__(256) void combine_kernel(RowsArgs a, int waves) {
   for (int64_t t = at.token; t < p.tokens; t += at.step) {
     int row = rows_of(p, t, 0);
     float weight = weights_of(a, t, 0, row);
-    for (int64_t c = at.column; c < a.cols; c += at.stride) {
+    for (int64_t c0 = at.column; c0 < a.cols; c0 += at.stride) {
+      const int64_t c = c0 + (threadIdx.x & 63) * 8;
       const int n = clamp8(a.cols - c);
       float s[8] = {};
       for (int k0 = 0; k0 < p.each; k0 += G) {
@@ -312,7 +327,7 @@ __global__ __launch_bounds__(256) void combine_kernel(RowsArgs a, int waves) {
 #pragma unroll
         for (int q = 0; q < G; ++q) {
           const int64_t r = at_lane(row, (k0 + q) & 63);
-          v[q] = raw8(y + (r < 0 ? 0 : r) * a.ldy + c, r >= 0 ? n : 0);
+          v[q] = raw8_once(y + (r < 0 ? 0 : r) * a.ldy + c, r >= 0 ? n : 0);
         }
 #pragma unroll
         for (int q = 0; q < G; ++q) {
@@ -348,7 +363,8 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(RowsArgs a, int w
       const int row = t < p.tokens ? rows_of(p, t, k0) : -1;
       const float weight = weights_of(a, t, k0, row);
       float sum[G] = {};
-      for (int64_t c = at.column; c < a.cols && t < p.tokens; c += at.stride) {
+      for (int64_t c0 = at.column; c0 < a.cols && t < p.tokens; c0 += at.stride) {
+        const int64_t c = c0 + lane * 8;
         const int n = clamp8(a.cols - c);
         float g[8];
         load8(g, d + t * a.ldx + c, n);
@@ -356,7 +372,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(RowsArgs a, int w
 #pragma unroll
         for (int q = 0; q < G; ++q) {
           const int64_t r = at_lane(row, q);
-          v[q] = raw8(y + (r < 0 ? 0 : r) * a.ldy + c, r >= 0 ? n : 0);
+          v[q] = raw8_once(y + (r < 0 ? 0 : r) * a.ldy + c, r >= 0 ? n : 0);
         }
 #pragma unroll
         for (int q = 0; q < G; ++q) {

@@ -24,14 +24,10 @@ __device__ __forceinline__ int tensor_of(const T* t, int count, unsigned block) 
 // What a block's scale byte stands for: 2^(byte - 127)
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte == 0 ? 1u << 22 : byte << 23); }
 
-// eight e4m3 codes as fp32
-__device__ __forceinline__ void decode8(float (&v)[8], uint2 c) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t w = h ? c.y : c.x;
-    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
-    v[4 * h] = lo[0], v[4 * h + 1] = lo[1], v[4 * h + 2] = hi[0], v[4 * h + 3] = hi[1];
-  }
+// four e4m3 codes as fp32
+__device__ __forceinline__ void decode4(float (&v)[4], uint32_t w) {
+  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
+  v[0] = lo[0], v[1] = lo[1], v[2] = hi[0], v[3] = hi[1];
 }
 
 // The e4m3 code of x, |x| inv <= 448: y = |x| inv in steps of its size (8 to 16
@@ -51,104 +47,153 @@ __device__ __forceinline__ uint32_t code_of(float x, float inv, float u) {
   return code | (__float_as_uint(x) >> 31 << 7);
 }
 
+// Four neighbouring elements at any place, the first n of them; a wave's lie side by
+// side, so that each access is of whole lines, and passes the caches by where
+// ONCE: nothing here is read again.
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef u16x4 u16x4_any __attribute__((aligned(2)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+
+template <typename T>
+__device__ __forceinline__ void load4(float (&v)[4], const T* p, int n) {
+  if (n >= 4) {
+    if constexpr (sizeof(T) == 4) {
+      const floatx4 x = __builtin_nontemporal_load(reinterpret_cast<const floatx4_any*>(p));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = x[j];
+    } else {
+      const u16x4 x = __builtin_nontemporal_load(reinterpret_cast<const u16x4_any*>(p));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = to_f32(__builtin_bit_cast(T, static_cast<uint16_t>(x[j])));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = j < n ? to_f32(p[j]) : 0.0f;
+  }
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4], int n) {
+  if (n >= 4) {
+    const floatx4 x = {v[0], v[1], v[2], v[3]};
+    __builtin_nontemporal_store(x, reinterpret_cast<floatx4_any*>(p));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) p[j] = v[j];
+  }
+}
+__device__ __forceinline__ uint32_t codes4_at(const uint8_t* p, int n) {
+  if (n >= 4) return __builtin_nontemporal_load(reinterpret_cast<const u32_any*>(p));
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < n) w |= static_cast<uint32_t>(p[j]) << (8 * j);
+  return w;
+}
+
+// four values of a block of 128, which 32 neighbouring lanes hold
 template <bool UP>
-__device__ __forceinline__ void round8(const float (&x)[8], const uint32_t (&h)[8], uint8_t* codes, uint8_t* scale, int n) {
+__device__ __forceinline__ void round4(const float (&x)[4], const uint32_t (&h)[4], uint8_t* codes, uint8_t* scale, int n) {
   uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max_u32(top, finite_abs(x[j]));
-  const uint32_t byte = scale_byte<OKLS_E4M3>(max16(top));
+  for (int j = 0; j < 4; ++j) top = max_u32(top, finite_abs(x[j]));
+  top = max16(top);
+  top = max_u32(top, static_cast<uint32_t>(__builtin_amdgcn_ds_swizzle(static_cast<int>(top), 0x401f)));    // the lane 16 further on, or back
+  const uint32_t byte = scale_byte<OKLS_E4M3>(top);
   const float inv = scale_inverse(byte);
-  uint32_t w[2] = {0, 0};
+  uint32_t w = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     const uint32_t half = UP ? h[j] >> 16 : h[j] & 0xffffu;
-    w[j >> 2] |= code_of<UP>(x[j], inv, static_cast<float>(half) * 0x1p-16f) << (8 * (j & 3));
+    w |= code_of<UP>(x[j], inv, static_cast<float>(half) * 0x1p-16f) << (8 * j);
   }
-  if (n == 8) {
-    typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    *reinterpret_cast<u32x2_any*>(codes) = u32x2{w[0], w[1]};
+  if (n >= 4) {
+    __builtin_nontemporal_store(w, reinterpret_cast<u32_any*>(codes));
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) codes[j] = static_cast<uint8_t>(w[j >> 2] >> (8 * (j & 3)));
+    for (int j = 0; j < 4; ++j)
+      if (j < n) codes[j] = static_cast<uint8_t>(w >> (8 * j));
   }
-  if ((threadIdx.x & 15) == 0 && n > 0) *scale = static_cast<uint8_t>(byte);
+  if ((threadIdx.x & 31) == 0 && n > 0) *scale = static_cast<uint8_t>(byte);
 }
 
-__device__ __forceinline__ uint2 codes_at(const uint8_t* codes, int n) {
-  typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
-  if (n == 8) {
-    const u32x2_any w = *reinterpret_cast<const u32x2_any*>(codes);
-    return uint2{w[0], w[1]};
-  }
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < n) w[j >> 2] |= static_cast<uint32_t>(codes[j]) << (8 * (j & 3));
-  return uint2{w[0], w[1]};
-}
+__device__ __forceinline__ int clamp4(int64_t left) { return left >= 4 ? 4 : left > 0 ? static_cast<int>(left) : 0; }
 
-// One thread's eight elements.  The gradient's type is known here, so that every
-// load is on its way before the first is used.
+// A thread's elements, kAdamParts times four of them.  The gradient's type is known here,
+// so that every load is on its way before the first is used.
+constexpr int kAdamParts = kAdamChunk / 1024;
 template <typename G, bool EIGHT>
-__device__ __forceinline__ void adamw8(const AdamArgs& a, const AdamTensor& t, int64_t i, int n, float factor) {
-  float p[8], g[8], m[8], v[8], s[8];
-  const int64_t blocks = (t.n + 127) >> 7, block = i >> 7;
-  load8(p, t.p + i, n);
-  const Raw8<G> raw = raw8(static_cast<const G*>(t.g) + i, n);
-  if constexpr (EIGHT) {
-    const float scale_m = n > 0 ? scale_value(t.scales[block]) : 0.0f, scale_s = n > 0 ? scale_value(t.scales[blocks + block]) : 0.0f;
-    decode8(m, codes_at(static_cast<const uint8_t*>(t.m) + i, n));
-    decode8(s, codes_at(static_cast<const uint8_t*>(t.v) + i, n));
+__device__ __forceinline__ void adamw_part(const AdamArgs& a, const AdamTensor& t, int64_t first, float factor) {
+  constexpr int Q = kAdamParts;
+  float p[Q][4], g[Q][4], m[Q][4], v[Q][4], s[Q][4], scale_m[Q], scale_s[Q];
+  uint32_t cm[Q], cs[Q];
+  const int64_t blocks = (t.n + 127) >> 7;
+  uint8_t *codes_m = static_cast<uint8_t*>(t.m), *codes_s = static_cast<uint8_t*>(t.v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = m[j] * scale_m;
-      s[j] = s[j] * scale_s;
-      v[j] = s[j] * s[j];
+  for (int q = 0; q < Q; ++q) {
+    const int64_t i = first + q * 1024;
+    const int n = clamp4(t.n - i);
+    load4(p[q], t.p + i, n);
+    load4(g[q], static_cast<const G*>(t.g) + i, n);
+    if constexpr (EIGHT) {
+      scale_m[q] = n > 0 ? scale_value(t.scales[i >> 7]) : 0.0f;
+      scale_s[q] = n > 0 ? scale_value(t.scales[blocks + (i >> 7)]) : 0.0f;
+      cm[q] = codes4_at(codes_m + i, n);
+      cs[q] = codes4_at(codes_s + i, n);
+    } else {
+      load4(m[q], static_cast<const float*>(t.m) + i, n);
+      load4(v[q], static_cast<const float*>(t.v) + i, n);
     }
-  } else {
-    load8(m, static_cast<const float*>(t.m) + i, n);
-    load8(v, static_cast<const float*>(t.v) + i, n);
   }
-  widen8(g, raw);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (a.norm != nullptr) g[j] = g[j] * factor;
-    m[j] = a.beta1 * m[j] + a.rest1 * g[j];
-    v[j] = a.beta2 * v[j] + a.rest2 * g[j] * g[j];
-    s[j] = __fsqrt_rn(v[j]);
-    p[j] = p[j] * a.decay - a.step * (m[j] / (s[j] * a.unbias2 + a.eps));
-  }
-  store8(t.p + i, p, n);
-  if constexpr (EIGHT) {
-    uint32_t h[8];
+  for (int q = 0; q < Q; ++q) {
+    const int64_t i = first + q * 1024;
+    const int n = clamp4(t.n - i);
+    if constexpr (EIGHT) {
+      decode4(m[q], cm[q]);
+      decode4(s[q], cs[q]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint64_t e = static_cast<uint64_t>(i + j);
-      uint32_t x = static_cast<uint32_t>(e) * 0x9E3779B9u + static_cast<uint32_t>(e >> 32) * 0x3C6EF372u + t.key;
-      x = (x ^ x >> 16) * 0x6A09E667u;
-      x = (x ^ x >> 15) * 0xBB67AE85u;
-      h[j] = x ^ x >> 16;
-      // past the tensor's end nothing joins the block's maximum
-      if (j >= n) m[j] = s[j] = 0.0f;
+      for (int j = 0; j < 4; ++j) {
+        m[q][j] = m[q][j] * scale_m[q];
+        s[q][j] = s[q][j] * scale_s[q];
+        v[q][j] = s[q][j] * s[q][j];
+      }
     }
-    round8<false>(m, h, static_cast<uint8_t*>(t.m) + i, t.scales + block, n);
-    round8<true>(s, h, static_cast<uint8_t*>(t.v) + i, t.scales + blocks + block, n);
-  } else {
-    store8(static_cast<float*>(t.m) + i, m, n);
-    store8(static_cast<float*>(t.v) + i, v, n);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (a.norm != nullptr) g[q][j] = g[q][j] * factor;
+      m[q][j] = a.beta1 * m[q][j] + a.rest1 * g[q][j];
+      v[q][j] = a.beta2 * v[q][j] + a.rest2 * g[q][j] * g[q][j];
+      s[q][j] = __fsqrt_rn(v[q][j]);
+      p[q][j] = p[q][j] * a.decay - a.step * (m[q][j] / (s[q][j] * a.unbias2 + a.eps));
+    }
+    store4(t.p + i, p[q], n);
+    if constexpr (EIGHT) {
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t e = static_cast<uint64_t>(i + j);
+        uint32_t x = static_cast<uint32_t>(e) * 0x9E3779B9u + static_cast<uint32_t>(e >> 32) * 0x3C6EF372u + t.key;
+        x = (x ^ x >> 16) * 0x6A09E667u;
+        x = (x ^ x >> 15) * 0xBB67AE85u;
+        h[j] = x ^ x >> 16;
+        // past the tensor's end nothing joins the block's maximum
+        if (j >= n) m[q][j] = s[q][j] = 0.0f;
+      }
+      round4<false>(m[q], h, codes_m + i, t.scales + (i >> 7), n);
+      round4<true>(s[q], h, codes_s + i, t.scales + blocks + (i >> 7), n);
+    } else {
+      store4(static_cast<float*>(t.m) + i, m[q], n);
+      store4(static_cast<float*>(t.v) + i, v[q], n);
+    }
   }
 }
 
-// 2048 elements of one tensor a workgroup, eight a thread: a block of 128 is 16
-// neighbouring lanes.
+// kAdamChunk elements of one tensor a workgroup.
 template <bool EIGHT>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
   const int at = __builtin_amdgcn_readfirstlane(tensor_of(a.tensor, a.count, blockIdx.x));
   const AdamTensor& t = a.tensor[at];
-  const int64_t i = static_cast<int64_t>(blockIdx.x - t.first) * kAdamChunk + threadIdx.x * 8;
-  const int n = clamp8(t.n - i);
+  const int64_t first = static_cast<int64_t>(blockIdx.x - t.first) * kAdamChunk + threadIdx.x * 4;
   float factor = 1.0f;
   if (a.norm != nullptr) {
     const float norm = *a.norm;
@@ -157,9 +202,9 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
     factor = static_cast<float>(f < 1.0 ? f : 1.0);
   }
   const int dtype = a.dtype[at];
-  if (dtype == OKLS_F32) adamw8<float, EIGHT>(a, t, i, n, factor);
-  else if (dtype == OKLS_BF16) adamw8<bf16_t, EIGHT>(a, t, i, n, factor);
-  else adamw8<half_t, EIGHT>(a, t, i, n, factor);
+  if (dtype == OKLS_F32) adamw_part<float, EIGHT>(a, t, first, factor);
+  else if (dtype == OKLS_BF16) adamw_part<bf16_t, EIGHT>(a, t, first, factor);
+  else adamw_part<half_t, EIGHT>(a, t, first, factor);
 }
 
 template <int THREADS>

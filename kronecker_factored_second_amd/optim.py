@@ -13,7 +13,10 @@ library on the current stream, and there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import itertools
+import operator
 from typing import NamedTuple, Optional
 
 import torch
@@ -85,20 +88,50 @@ def grad_norm(grads) -> torch.Tensor:
     grads = [g if g.is_contiguous() else g.contiguous() for g in grads]
     if not grads:
         raise ValueError("no gradients")
-    device, index, dtypes, flat = grads[0].device, grads[0].get_device(), linear.DTYPES, []
-    for i, g in enumerate(grads):
-        dtype = dtypes.get(g.dtype)
-        if dtype is None:
-            raise ValueError(f"gradient {i} must be float32, bfloat16 or float16, got {g.dtype}")
-        if g.get_device() != index or index < 0:
-            raise ValueError(f"gradient {i} is on {g.device}, the first on {device}: all must be on one GPU")
-        flat += (g.data_ptr(), g.numel(), dtype)
-    table = (ctypes.c_uint64 * len(flat))(*flat)        # of GradientStruct
-    need = (_lib or load()).okls_grad_norm_workspace_size(len(grads), table)
+    device, index, dtypes = grads[0].device, grads[0].get_device(), linear.DTYPES
+    codes = [dtypes.get(g.dtype) for g in grads]
+    if None in codes or index < 0 or set(map(_device, grads)) != {index}:
+        for i, g in enumerate(grads):
+            if codes[i] is None:
+                raise ValueError(f"gradient {i} must be float32, bfloat16 or float16, got {g.dtype}")
+            if g.get_device() != index or index < 0:
+                raise ValueError(f"gradient {i} is on {g.device}, the first on {device}: all must be on one GPU")
+    table = array.array("Q", itertools.chain.from_iterable(zip(map(_address, grads), map(_numel, grads), codes)))      # of GradientStruct
+    at = table.buffer_info()[0]
+    need = (_lib or load()).okls_grad_norm_workspace_size(len(grads), at)
     ws = torch.empty(need, dtype=torch.uint8, device=device)
     norm = torch.empty((), dtype=torch.float32, device=device)
-    _on(device, "okls_grad_norm", len(grads), table, norm.data_ptr(), ws.data_ptr() if need else None, need)
+    _on(device, "okls_grad_norm", len(grads), at, norm.data_ptr(), ws.data_ptr() if need else None, need)
     return norm
+
+
+_numel, _address, _device, _contiguous = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.get_device, torch.Tensor.is_contiguous
+_dtype = operator.attrgetter("dtype")
+
+
+def _scales_fit(s, n, index, eight):
+    if not eight or s is None:
+        return not eight and s is None
+    return s.dtype is torch.float8_e8m0fnu and s.shape == (2, -(-n // 128)) and s.get_device() == index and s.is_contiguous()
+
+
+def _refuse(params, grads, moments, index, device, held, eight):
+    """Raises for the first tensor that is not as `adamw` says."""
+    for i, (p, g, (m, v, scales)) in enumerate(zip(params, grads, moments)):
+        n = p.numel()
+        if p.dtype is not torch.float32 or p.get_device() != index or not p.is_contiguous():
+            raise ValueError(f"parameter {i} must be a contiguous float32 tensor on {device}, got {p.dtype} on {p.device}")
+        if g is None or g.dtype not in linear.DTYPES:
+            raise ValueError(f"gradient {i} must be float32, bfloat16 or float16, got {'none' if g is None else g.dtype}")
+        if not g.is_same_size(p) or g.get_device() != index:
+            raise ValueError(f"gradient {i} is {tuple(g.shape)} on {g.device}, parameter {tuple(p.shape)} on {device}")
+        if any(x.dtype is not held or x.numel() != n or x.get_device() != index or not x.is_contiguous() for x in (m, v)):
+            raise ValueError(f"moments {i} must be contiguous {held} tensors of {n} elements on {device}, got "
+                             f"{tuple(m.shape)} {m.dtype} on {m.device} and {tuple(v.shape)} {v.dtype} on {v.device}")
+        if not _scales_fit(scales, n, index, eight):
+            raise ValueError(f"scales {i} must be {f'contiguous float8_e8m0fnu {(2, -(-n // 128))} on {device}' if eight else 'None'}, "
+                             f"got {None if scales is None else (scales.dtype, tuple(scales.shape), scales.device)}")
+    raise ValueError("parameters, gradients and moments do not fit")
 
 
 def adamw(params, grads, moments, t, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, norm=None, max_norm=None):
@@ -122,41 +155,32 @@ def adamw(params, grads, moments, t, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, 
     device, index, dtypes, float32 = params[0].device, params[0].get_device(), linear.DTYPES, torch.float32
     if index < 0:
         raise ValueError(f"parameter 0 must be on a GPU, got {device}")
-    eight = moments[0][2] is not None
+    ms, vs, scales = zip(*moments)
+    eight = scales[0] is not None
     held = torch.float8_e4m3fn if eight else float32
-    flat, kept = [], []
-    for i, (p, g, (m, v, scales)) in enumerate(zip(params, grads, moments)):
-        n = p.numel()
-        if p.dtype is not float32 or p.get_device() != index or not p.is_contiguous():
-            raise ValueError(f"parameter {i} must be a contiguous float32 tensor on {device}, got {p.dtype} on {p.device}")
-        dtype = None if g is None else dtypes.get(g.dtype)
-        if dtype is None:
-            raise ValueError(f"gradient {i} must be float32, bfloat16 or float16, got {'none' if g is None else g.dtype}")
-        if not g.is_same_size(p) or g.get_device() != index:
-            raise ValueError(f"gradient {i} is {tuple(g.shape)} on {g.device}, parameter {tuple(p.shape)} on {device}")
-        if not g.is_contiguous():
-            g = g.contiguous()
-            kept.append(g)
-        if (m.dtype is not held or v.dtype is not held or m.numel() != n or v.numel() != n or m.get_device() != index
-                or v.get_device() != index or not m.is_contiguous() or not v.is_contiguous()):
-            raise ValueError(f"moments {i} must be contiguous {held} tensors of {n} elements on {device}, got "
-                             f"{tuple(m.shape)} {m.dtype} on {m.device} and {tuple(v.shape)} {v.dtype} on {v.device}")
-        if (scales is not None) != eight or (eight and (scales.dtype is not torch.float8_e8m0fnu or scales.shape != (2, -(-n // 128))
-                                                        or scales.get_device() != index or not scales.is_contiguous())):
-            raise ValueError(f"scales {i} must be {f'contiguous float8_e8m0fnu {(2, -(-n // 128))} on {device}' if eight else 'None'}, "
-                             f"got {None if scales is None else (scales.dtype, tuple(scales.shape), scales.device)}")
-        flat += (p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), scales.data_ptr() if eight else 0, n, dtype)
-    table = (ctypes.c_uint64 * len(flat))(*flat)        # of TensorStruct
-    places = [at for at, n in zip(flat[::7], flat[5::7]) if n]
-    if len(set(places)) != len(places):
-        raise ValueError("a parameter is in the list twice")
+    counts = list(map(_numel, params))
+    # all at once where everything is as it should be; one by one to say what is not
+    grads = [g if g is None or g.is_contiguous() else g.contiguous() for g in grads]
+    codes = [None if g is None else dtypes.get(g.dtype) for g in grads]
+    if (None in codes or set(map(_dtype, params)) != {float32} or set(map(_dtype, ms + vs)) != {held}
+            or {*map(_device, params), *map(_device, grads), *map(_device, ms), *map(_device, vs)} != {index}
+            or not all(map(_contiguous, params)) or not all(map(_contiguous, ms)) or not all(map(_contiguous, vs))
+            or not all(map(torch.Tensor.is_same_size, grads, params)) or list(map(_numel, ms)) != counts or list(map(_numel, vs)) != counts
+            or not all(_scales_fit(s, n, index, eight) for s, n in zip(scales, counts))):
+        _refuse(params, grads, moments, index, device, held, eight)
+    places, m_places, v_places = list(map(_address, params)), list(map(_address, ms)), list(map(_address, vs))
+    every = places + m_places + v_places
+    if len(set(every)) != len(every) and len({a for a, n in zip(every, counts * 3) if n}) != 3 * sum(n > 0 for n in counts):
+        raise ValueError("a parameter or one of its moments is in the lists twice")
+    rows = zip(places, map(_address, grads), m_places, v_places, map(_address, scales) if eight else itertools.repeat(0), counts, codes)
+    table = array.array("Q", itertools.chain.from_iterable(rows))        # of TensorStruct
     if norm is not None:
         if norm.dtype != float32 or norm.numel() != 1 or norm.device != device:
             raise ValueError(f"norm must be one float32 on {device}, got {tuple(norm.shape)} {norm.dtype} on {norm.device}")
         if max_norm is None:
             raise ValueError("norm needs max_norm")
     config = ConfigStruct(lr, beta1, beta2, eps, weight_decay, max_norm if norm is not None else 0.0, 8 if eight else 32)
-    _on(device, "okls_adamw", config, t, len(params), table, None if norm is None else norm.data_ptr())
+    _on(device, "okls_adamw", config, t, len(params), table.buffer_info()[0], None if norm is None else norm.data_ptr())
     # a graph that kept one has to know, as of torch's own writes
     linear._written([p for p in params if not p.is_inference()])
 

@@ -264,7 +264,7 @@ def test_refusals():
                 dict(grads=[g.cpu()]), dict(grads=[g.double()]), dict(moments=[optim.Moments(m.m, m.v[:299])]), dict(moments=[optim.Moments(m.m.half(), m.v)]),
                 dict(moments=[optim.Moments(e.m, e.v)]), dict(moments=[optim.Moments(m.m, m.v, e.scales)]), dict(moments=[optim.Moments(e.m, e.v, e.scales[:1])]),
                 dict(moments=[optim.Moments(e.m, e.v, e.scales.view(torch.uint8))]), dict(params=[p, p], grads=[g, g], moments=[m, optim.new_moments(p)]),
-                dict(params=[p, g], grads=[g, g], moments=[m, e]), dict(norm=torch.ones(2, device="cuda"), max_norm=1.0), dict(norm=torch.ones(1), max_norm=1.0),
+                dict(params=[p, g], grads=[g, g], moments=[m, e]), dict(params=[p, g], grads=[g, g], moments=[m, m]), dict(moments=[optim.Moments(m.m, m.m)]), dict(norm=torch.ones(2, device="cuda"), max_norm=1.0), dict(norm=torch.ones(1), max_norm=1.0),
                 dict(norm=torch.ones((), device="cuda"))):
         with pytest.raises(ValueError):
             optim.adamw(**{**dict(params=[p], grads=[g], moments=[m], t=1), **bad})
