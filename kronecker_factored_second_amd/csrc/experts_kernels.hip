@@ -507,19 +507,47 @@ __device__ __forceinline__ TileJob expert_job(const ExpertMatmulArgs& a, const T
 
 constexpr int kTailGroups = 64;    // more workgroups than tiles, so that some write the zeros
 
-template <class C, int FA, int FB, bool F32>
-__global__ __launch_bounds__(C::NT, 2) void expert_tile_kernel(ExpertMatmulArgs a, unsigned tn) {
+// Large tiles are one workgroup a CU.  What is left over after whole rounds of all
+// CUs, where it is at most half a round, goes to a launch of small tiles, four of which
+// are a large one and two of which a CU holds: 16384 uneven rows x 2048 x 5632 193 ->
+// 177 us.  A round of short sums costs less than the launch (64 experts, 32764 rows x
+// 2816 x 1024: 157 -> 164 us), so that it is made from a summed axis of kLongSum on.
+constexpr unsigned kRound = 256;
+constexpr int64_t kLongSum = 4096;
+__device__ __forceinline__ unsigned whole_rounds(unsigned total) {
+  return total % kRound <= kRound / 2 ? total - total % kRound : total;
+}
+
+// tile t's rows, and its column of tiles: bands of 8 tile rows, column by column
+template <class C>
+__device__ __forceinline__ TileJob tile_job(const ExpertMatmulArgs& a, unsigned t, unsigned tm, unsigned tn, int upto) {
   auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-  int upto;
-  const unsigned tm = count_tiles<C::BM>(a.plan, upto), total = tm * tn, w = blockIdx.x, x = w & 7;
-  if (w >= total) return zero_tail(a, w - total, gridDim.x - total);
-  // as in the plain product: each XCD takes a run of neighbouring tiles in bands of 8 tile rows
-  const unsigned t = x * (total >> 3) + (x < (total & 7) ? x : (total & 7)) + (w >> 3);
   const unsigned band = uniform(t / (8u * tn)), in = t - band * 8u * tn;
   const unsigned high = tm - band * 8 < 8 ? tm - band * 8 : 8, column = uniform(in / high);
   TileJob o = expert_job(a, find_tile<C::BM>(a.plan, band * 8 + in - column * high, upto));
   o.n0 = static_cast<int64_t>(column) * C::BN;
-  tile_product<C, FA, FB, F32>(o);
+  return o;
+}
+
+template <class C, int FA, int FB, bool F32>
+__global__ __launch_bounds__(C::NT, 2) void expert_tile_kernel(ExpertMatmulArgs a, unsigned tn, bool rest_apart) {
+  int upto;
+  const unsigned tm = count_tiles<C::BM>(a.plan, upto), whole = rest_apart ? whole_rounds(tm * tn) : tm * tn, w = blockIdx.x, x = w & 7;
+  if (w >= whole) return zero_tail(a, w - whole, gridDim.x - whole);
+  // as in the plain product: each XCD takes a run of neighbouring tiles
+  tile_product<C, FA, FB, F32>(tile_job<C>(a, x * (whole >> 3) + (x < (whole & 7) ? x : (whole & 7)) + (w >> 3), tm, tn, upto));
+}
+
+template <int FA, int FB, bool F32>
+__global__ __launch_bounds__(TileSmall::NT, 2) void expert_rest_kernel(ExpertMatmulArgs a, unsigned tn) {
+  static_assert(TileBig::BM == 2 * TileSmall::BM && TileBig::BN == 2 * TileSmall::BN, "four small tiles are a large one");
+  int upto;
+  const unsigned tm = count_tiles<TileBig::BM>(a.plan, upto), total = tm * tn, t = whole_rounds(total) + (blockIdx.x >> 2);
+  if (t >= total) return;
+  TileJob o = tile_job<TileBig>(a, t, tm, tn, upto);
+  o.m0 += (blockIdx.x >> 1 & 1) * TileSmall::BM;
+  o.n0 += (blockIdx.x & 1) * TileSmall::BN;
+  if (o.m0 < o.m && o.n0 < o.n) tile_product<TileSmall, FA, FB, F32>(o);
 }
 
 // Few rows an expert: units of 32 rows and 64 columns, 16 a wave, an even share of
@@ -817,7 +845,7 @@ hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s) {
     auto tiles = [&](auto tile) {
       using C = decltype(tile);
       const unsigned tn = static_cast<unsigned>((a.n + C::BN - 1) / C::BN);
-      expert_tile_kernel<C, FA, FB, F32><<<most_tiles(p, C::BM) * tn + kTailGroups, C::NT, 0, s>>>(a, tn);
+      expert_tile_kernel<C, FA, FB, F32><<<most_tiles(p, C::BM) * tn + kTailGroups, C::NT, 0, s>>>(a, tn, C::NW == 8 && a.a.cols >= kLongSum);
     };
     if (each <= 8 || (each <= 32 && count(64, 128) < 200)) {
       const int64_t units = most_tiles(p, 32) * ((a.n + 63) / 64);
@@ -828,6 +856,7 @@ hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s) {
       tiles(TileSmall{});
     } else {
       tiles(TileBig{});
+      if (a.a.cols >= kLongSum) expert_rest_kernel<FA, FB, F32><<<4 * (kRound / 2), TileSmall::NT, 0, s>>>(a, static_cast<unsigned>((a.n + TileBig::BN - 1) / TileBig::BN));
     }
   });
   return hipGetLastError();

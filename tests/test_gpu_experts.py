@@ -295,6 +295,13 @@ def test_matmul(tokens, each, e, n, k, kind):
     _product(7, tokens, each, e, n, k, kind)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens,each,e,n,align", [(1700, 1, 5, 8000, 128), (1700, 1, 5, 6100, 16), (2000, 1, 4, 8192, 128), (2300, 1, 6, 7000, 128)])
+def test_matmul_long_sums(tokens, each, e, n, align, kind):
+    """From 4096 of the summed axis on, what whole rounds of large tiles leave goes to small ones: rests of less and of more than half a round."""
+    _product(22, tokens, each, e, n, 4096 + 130, kind, align=align, dropped=0.02)
+
+
 @pytest.mark.parametrize("align", [16, 32, 64])
 @pytest.mark.parametrize("tokens,each,e,n,k", [(8, 2, 8, 300, 700), (150, 2, 7, 300, 500), (400, 2, 6, 300, 256), (1400, 4, 20, 2500, 130)])
 def test_matmul_close_rows(tokens, each, e, n, k, align):
