@@ -623,10 +623,12 @@ __global__ __launch_bounds__(256) void expert_stream_kernel(ExpertMatmulArgs a) 
       aim();
     };
 
-    // Where a lane reads in a stage: its two 16-byte chunks of its row of b, and of a, and their scale bytes.
+    // Where a lane reads in a stage: two 16-byte chunks of its row of b, and of a, and their
+    // scale bytes.  Both operands take chunks `quarter` and `quarter` + 4, and a sum does not care which
+    // (2 quarter and the next one met in the banks).
     const int r = lane & 15, quarter = lane >> 4, sw = r >> 1 & 7;
     const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)ring));
-    const uint32_t lo = (2 * quarter ^ sw) << 4, hi = ((2 * quarter + 1) ^ sw) << 4;
+    const uint32_t lo = (quarter ^ sw) << 4, hi = ((quarter + 4) ^ sw) << 4;
     const uint32_t b_lo = base + (wave * 16 + r) * 128 + lo, b_hi = b_lo - lo + hi, a_lo = base + (64 + r) * 128 + lo, a_hi = a_lo - lo + hi;
     const uint32_t b_e = base + kStreamScales + wave * 16 + r, a_e = base + kStreamScales + 64 + r;
     floatx4 acc[2] = {};

@@ -142,7 +142,7 @@ def adamw(params, grads, moments, t, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, 
         v <- beta2 v + (1 - beta2) g^2
         p <- (1 - lr weight_decay) p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
 
-    Where norm is no finite number nothing is written.  8-bit moments are rounded
+    Where norm is no finite number nothing is written; without norm max_norm is not read.  8-bit moments are rounded
     up or down in proportion, by thresholds that t, the tensor's place in the list and
     the element's number give; the update takes them before they are rounded.
     Tensors may have any shape and be views; all must be contiguous, on one GPU
@@ -180,7 +180,7 @@ def adamw(params, grads, moments, t, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, 
         if max_norm is None:
             raise ValueError("norm needs max_norm")
     config = ConfigStruct(lr, beta1, beta2, eps, weight_decay, max_norm if norm is not None else 0.0, 8 if eight else 32)
-    _on(device, "okls_adamw", config, t, len(params), table.buffer_info()[0], None if norm is None else norm.data_ptr())
+    _on(device, "okls_adamw", config, operator.index(t), len(params), table.buffer_info()[0], None if norm is None else norm.data_ptr())
     # a graph that kept one has to know, as of torch's own writes
     linear._written([p for p in params if not p.is_inference()])
 

@@ -591,3 +591,27 @@ def test_training_steps_together():
         rest.zero_grad()
         assert all(t.isfinite().all() for t in (total, gate_up, down, router, norm))
     assert all(not torch.equal(t.detach(), s) for t, s in zip((gate_up, down, router, norm), start))
+
+
+def test_example_runs():
+    """The example's steps run, and its stack's gradients are the formula's: against the same blocks in fp32 without 8 bits, whose roundings are off by 2^-4 of each value at most."""
+    from examples import train_experts
+    losses = train_experts.train(steps=3, blocks=1, n_experts=4, d=64, f=64, tokens=200)
+    assert len(losses) == 3 and all(np.isfinite(losses))
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    (norm, router, gate_up, down), = train_experts.make(1, 4, 64, 64, gen, "cuda")
+    leaves = [t.requires_grad_() for t in (gate_up, down)]
+    x, dout = torch.randn(200, 64, generator=gen, device="cuda"), torch.randn(200, 64, generator=gen, device="cuda")
+    got = torch.autograd.grad(train_experts.forward([(norm, router, gate_up, down)], x, 2), leaves, dout)
+    U, D = (t.detach().double().cpu().requires_grad_() for t in leaves)
+    h = x * torch.rsqrt(x.square().mean(1, keepdim=True) + 1e-6) * norm
+    best, choice = (h @ router.T).topk(2)
+    H, V, C = h.double().cpu(), best.softmax(1).double().cpu(), choice.cpu()
+    ref = x.double().cpu()
+    for k in range(2):
+        gate, up = (U[C[:, k]] @ H[:, :, None])[..., 0].chunk(2, dim=1)
+        ref = ref + (D[C[:, k]] @ (torch.nn.functional.silu(gate) * up)[:, :, None])[..., 0] * V[:, k: k + 1]
+    want = torch.autograd.grad(ref, (U, D), dout.double().cpu())
+    for a, b in zip(got, want):
+        # products of two rounded factors, two layers deep, and the output's gradient in two bits of fraction
+        assert (a.double().cpu() - b).norm() < 2.0 ** -2 * b.norm()
