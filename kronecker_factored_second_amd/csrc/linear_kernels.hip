@@ -33,6 +33,7 @@ constexpr int kTileStride = 128 + 16;   // bytes; 16-byte rows that start at dif
 // order of experts' rows, zeros in rows without a choice.  Workgroups along y take
 // a stack's matrices.
 enum Source { kAsIs, kFactors, kSorted };
+typedef intx4 intx4_any __attribute__((aligned(4)));
 
 template <typename T, int FMT, int SOURCE>
 __global__ __launch_bounds__(256, SOURCE == kFactors ? 3 : 4) void quantize_kernel(QuantArgs a) {
@@ -52,10 +53,21 @@ __global__ __launch_bounds__(256, SOURCE == kFactors ? 3 : 4) void quantize_kern
     const int64_t r0 = br * 128 + rg * 8, c0 = bc * 128 + c8 * 8;
     const int nc = clamp8(a.cols - c0);
     Raw8<T> raw[8];
+    int pairs[SOURCE == kSorted ? 8 : 1];
+    if constexpr (SOURCE == kSorted) {
+      if (r0 + 8 <= a.rows) {
+        const auto* at = reinterpret_cast<const intx4_any*>(a.pairs + r0);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) pairs[p] = at[p >> 2][p & 3];
+      } else {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) pairs[p] = r0 + p < a.rows ? a.pairs[r0 + p] : -1;
+      }
+    }
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       if constexpr (SOURCE == kSorted) {
-        const int pair = r0 + p < a.rows ? a.pairs[r0 + p] : -1;
+        const int pair = pairs[p];
         const bool some = pair >= 0 && pair < a.n_pairs;
         const int64_t row = !some ? 0 : a.each > 0 ? pair / a.each : r0 + p;
         raw[p] = raw8(x + row * a.ldx + c0, some ? nc : 0);
