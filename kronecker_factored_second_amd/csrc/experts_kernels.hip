@@ -421,14 +421,6 @@ __device__ __forceinline__ void expert_rows(const ExpertPlan& p, int e, int& fir
   end = max(min(p.offsets[e + 1], p.capacity) & ~15, first);
 }
 
-// the same for an expert that is the same in all lanes, by a scalar load: a wait for it
-// does not wait for the copies under way
-__device__ __forceinline__ void one_experts_rows(const ExpertPlan& p, int e, int& first, int& end) {
-  const auto* offsets = (const __attribute__((address_space(4))) int32_t*)p.offsets;
-  first = min(max(offsets[e], 0), p.capacity) & ~15;
-  end = max(min(offsets[e + 1], p.capacity) & ~15, first);
-}
-
 // v summed over this lane and those before it, inside the ALU: within each 16
 // lanes, then from row to row
 __device__ __forceinline__ int sum_up_to(int v) {
@@ -442,38 +434,45 @@ __device__ __forceinline__ int sum_up_to(int v) {
   return v + from(v, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});
 }
 
-// the tiles of experts e0 + 0 .. e0 + lane
+// 64 experts, one a lane: its rows, and the tiles of BM rows of it and those before it
+struct ExpertLanes {
+  int first, end, upto;
+};
 template <int BM>
-__device__ __forceinline__ int tiles_up_to(const ExpertPlan& p, int e0) {
+__device__ __forceinline__ ExpertLanes expert_lanes(const ExpertPlan& p, int e0) {
   const int e = e0 + (threadIdx.x & 63);
-  int first = 0, end = 0;
-  if (e < p.n_experts) expert_rows(p, e, first, end);
-  return sum_up_to((end - first + BM - 1) / BM);
+  ExpertLanes x{0, 0, 0};
+  if (e < p.n_experts) expert_rows(p, e, x.first, x.end);
+  x.upto = sum_up_to((x.end - x.first + BM - 1) / BM);
+  return x;
 }
 
-// The tiles of all experts; `upto` is tiles_up_to of the first 64.
+// The tiles of all experts; `x` is expert_lanes of the first 64, whose offsets are read once.
 template <int BM>
-__device__ __forceinline__ int count_tiles(const ExpertPlan& p, int& upto) {
-  upto = tiles_up_to<BM>(p, 0);
-  int total = __builtin_amdgcn_readlane(upto, 63);
-  for (int e0 = 64; e0 < p.n_experts; e0 += 64) total += __builtin_amdgcn_readlane(tiles_up_to<BM>(p, e0), 63);
+__device__ __forceinline__ int count_tiles(const ExpertPlan& p, ExpertLanes& x) {
+  x = expert_lanes<BM>(p, 0);
+  int total = __builtin_amdgcn_readlane(x.upto, 63);
+  for (int e0 = 64; e0 < p.n_experts; e0 += 64) total += __builtin_amdgcn_readlane(expert_lanes<BM>(p, e0).upto, 63);
   return total;
 }
 
 // tile t < count_tiles
 template <int BM>
-__device__ __forceinline__ TileRows find_tile(const ExpertPlan& p, int t, int upto) {
+__device__ __forceinline__ TileRows find_tile(const ExpertPlan& p, int t, ExpertLanes x) {
   TileRows r{0, 0, 0};
   int before = 0;
   for (int e0 = 0; e0 < p.n_experts; e0 += 64) {
-    if (e0 != 0) upto = tiles_up_to<BM>(p, e0) + before;
-    const int all = __builtin_amdgcn_readlane(upto, 63);
+    if (e0 != 0) {
+      x = expert_lanes<BM>(p, e0);
+      x.upto += before;
+    }
+    const int all = __builtin_amdgcn_readlane(x.upto, 63);
     if (t < all) {
-      const int lane = __popcll(__ballot(upto <= t));     // experts that end at or before t
-      const int begin = lane == 0 ? before : __builtin_amdgcn_readlane(upto, lane - 1);
-      r.expert = __builtin_amdgcn_readfirstlane(e0 + lane);
-      one_experts_rows(p, r.expert, r.first, r.end);
-      r.first += (t - begin) * BM;
+      const int lane = __popcll(__ballot(x.upto <= t));     // experts that end at or before t
+      const int begin = lane == 0 ? before : __builtin_amdgcn_readlane(x.upto, lane - 1);
+      r.expert = e0 + lane;
+      r.first = __builtin_amdgcn_readlane(x.first, lane) + (t - begin) * BM;
+      r.end = __builtin_amdgcn_readlane(x.end, lane);
       break;
     }
     before = all;
@@ -520,34 +519,34 @@ __device__ __forceinline__ unsigned whole_rounds(unsigned total) {
 
 // tile t's rows, and its column of tiles: bands of 8 tile rows, column by column
 template <class C>
-__device__ __forceinline__ TileJob tile_job(const ExpertMatmulArgs& a, unsigned t, unsigned tm, unsigned tn, int upto) {
+__device__ __forceinline__ TileJob tile_job(const ExpertMatmulArgs& a, unsigned t, unsigned tm, unsigned tn, const ExpertLanes& lanes) {
   auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
   const unsigned band = uniform(t / (8u * tn)), in = t - band * 8u * tn;
   const unsigned high = tm - band * 8 < 8 ? tm - band * 8 : 8, column = uniform(in / high);
-  TileJob o = expert_job(a, find_tile<C::BM>(a.plan, band * 8 + in - column * high, upto));
+  TileJob o = expert_job(a, find_tile<C::BM>(a.plan, band * 8 + in - column * high, lanes));
   o.n0 = static_cast<int64_t>(column) * C::BN;
   return o;
 }
 
 template <class C, int FA, int FB, bool F32>
 __global__ __launch_bounds__(C::NT, 2) void expert_tile_kernel(ExpertMatmulArgs a, unsigned tn, bool rest_apart) {
-  int upto;
-  const unsigned tm = count_tiles<C::BM>(a.plan, upto), whole = rest_apart ? whole_rounds(tm * tn) : tm * tn, w = blockIdx.x, x = w & 7;
+  ExpertLanes lanes;
+  const unsigned tm = count_tiles<C::BM>(a.plan, lanes), whole = rest_apart ? whole_rounds(tm * tn) : tm * tn, w = blockIdx.x, x = w & 7;
   if (w >= whole) return zero_tail(a, w - whole, gridDim.x - whole);
   // as in the plain product: each XCD takes a run of neighbouring tiles
-  tile_product<C, FA, FB, F32>(tile_job<C>(a, x * (whole >> 3) + (x < (whole & 7) ? x : (whole & 7)) + (w >> 3), tm, tn, upto));
+  tile_product<C, FA, FB, F32, true>(tile_job<C>(a, x * (whole >> 3) + (x < (whole & 7) ? x : (whole & 7)) + (w >> 3), tm, tn, lanes));
 }
 
 template <int FA, int FB, bool F32>
 __global__ __launch_bounds__(TileSmall::NT, 2) void expert_rest_kernel(ExpertMatmulArgs a, unsigned tn) {
   static_assert(TileBig::BM == 2 * TileSmall::BM && TileBig::BN == 2 * TileSmall::BN, "four small tiles are a large one");
-  int upto;
-  const unsigned tm = count_tiles<TileBig::BM>(a.plan, upto), total = tm * tn, t = whole_rounds(total) + (blockIdx.x >> 2);
+  ExpertLanes lanes;
+  const unsigned tm = count_tiles<TileBig::BM>(a.plan, lanes), total = tm * tn, t = whole_rounds(total) + (blockIdx.x >> 2);
   if (t >= total) return;
-  TileJob o = tile_job<TileBig>(a, t, tm, tn, upto);
+  TileJob o = tile_job<TileBig>(a, t, tm, tn, lanes);
   o.m0 += (blockIdx.x >> 1 & 1) * TileSmall::BM;
   o.n0 += (blockIdx.x & 1) * TileSmall::BN;
-  if (o.m0 < o.m && o.n0 < o.n) tile_product<TileSmall, FA, FB, F32>(o);
+  if (o.m0 < o.m && o.n0 < o.n) tile_product<TileSmall, FA, FB, F32, true>(o);
 }
 
 // Few rows an expert: units of 32 rows and 64 columns, 16 a wave, an even share of
@@ -565,8 +564,8 @@ __global__ __launch_bounds__(256) void expert_stream_kernel(ExpertMatmulArgs a) 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int blocks = static_cast<int>((a.a.cols + 127) >> 7);
   const unsigned columns = static_cast<unsigned>((a.n + 63) >> 6);
-  int upto;
-  const int tm = count_tiles<32>(a.plan, upto);
+  ExpertLanes lanes;
+  const int tm = count_tiles<32>(a.plan, lanes);
   const uint64_t units = static_cast<uint64_t>(tm) * columns, unit = units * blockIdx.x / gridDim.x;
   const int64_t steps = static_cast<int64_t>(units * (blockIdx.x + 1) / gridDim.x - unit) * blocks;
 
@@ -577,7 +576,7 @@ __global__ __launch_bounds__(256) void expert_stream_kernel(ExpertMatmulArgs a) 
     // read the last one; what they give is not stored.  Scale bytes: one copy, by every
     // wave to the same place.
     unsigned tile = static_cast<unsigned>(unit / columns), column = static_cast<unsigned>(unit - static_cast<uint64_t>(tile) * columns);
-    TileRows rows = find_tile<32>(a.plan, tile, upto);
+    TileRows rows = find_tile<32>(a.plan, tile, lanes);
     const int chunk = lane & 7, in = lane >> 3;
     const uint8_t *pa, *pb[2], *pe;
     const bool of_b = lane < 16;
@@ -618,7 +617,7 @@ __global__ __launch_bounds__(256) void expert_stream_kernel(ExpertMatmulArgs a) 
       block = 0;
       if (++column == columns) {
         column = 0;
-        rows = find_tile<32>(a.plan, ++tile, upto);
+        rows = find_tile<32>(a.plan, ++tile, lanes);
       }
       aim();
     };
@@ -688,7 +687,7 @@ __global__ __launch_bounds__(256) void expert_stream_kernel(ExpertMatmulArgs a) 
       }
       if (++here_column == columns && s + 1 < steps) {
         here_column = 0;
-        here = find_tile<32>(a.plan, ++here_tile, upto);
+        here = find_tile<32>(a.plan, ++here_tile, lanes);
       }
     }
     WAIT_VM(0);              // the last copies land before the LDS is given up

@@ -118,7 +118,9 @@ struct TileJob {
 template <int N> struct ScaleWord { using type = uint32_t; };
 template <> struct ScaleWord<2> { using type = uint16_t; };
 
-template <class C, int FA, int FB, bool F32>
+// UNEVEN: tiles that end early are common, and a wave whose rows all lie behind the end
+// copies its part and leaves the products to the others.
+template <class C, int FA, int FB, bool F32, bool UNEVEN = false>
 __device__ __forceinline__ void tile_product(const TileJob& o) {
   constexpr int GI = C::GI, GJ = C::GJ;
   constexpr int P = F32 ? 4 : 2;          // parts of a stage of 128 of k
@@ -384,6 +386,17 @@ __device__ __forceinline__ void tile_product(const TileJob& o) {
     for (int j = 0; j < GJ; ++j) acc[i][j] = floatx16{};
   WAIT_VM(C::LA + C::LB + 1);
   barrier();
+  if (UNEVEN && m0 + wm * C::RM >= m) {
+    for (int st = 0; st < nst; ++st) {
+      WAIT_VM(0);
+      barrier();
+      if (st & 1) copy(sA1, sB1, e1);
+      else copy(sA0, sB0, e0);
+    }
+    WAIT_VM(0);
+    if constexpr (C::NW == 8) barrier();
+    return;
+  }
   fetch(I0{}, sA0, sB0, e0);
   for (int st = 0; st < nst; st += 2) {
     stage(I0{});
