@@ -19,8 +19,9 @@ namespace {
 // of them in turn, 64 at a time: lanes with the same expert find each other by one
 // ballot for each bit of its number, the count so far is the wave's own in LDS.
 // Then the counts of the waves, groups and workgroups before are added.
-// Bound by latency: 65536 choices of 64 experts take two launches of 6 us; up to
-// 4096 choices one workgroup does it all in 4 us.
+// Bound by latency: 65536 choices of 64 experts take two launches of 7 and 6.5 us (in
+// three launches with ranks kept in memory it took 24); up to 4096 choices one
+// workgroup does it all in 4 us.
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanEach = 4, kPlanGroup = kPlanThreads * kPlanEach;
 constexpr int kPlanBlocks = 64;         // workgroups at most: each adds up the counts of all
@@ -202,9 +203,14 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const void* ch
 // ---------------------------------------------------------------------------
 // Rows to the sorted order and back
 // ---------------------------------------------------------------------------
-// A token's row by a wave, its parts of 512 columns by gridDim.y waves in turn.
 // Tokens lead in every direction: a token's row is read (written) once for all
 // its choices.  The first workgroups write the zeros of rows without a choice.
+// Bound by memory.  8192 tokens of 8 choices, 2048 columns of bf16: to the sorted order
+// (335 MB) 54 us, 6.2 TB/s; back (302 MB) 48 us, 6.3 TB/s; the gradient (603 MB) 121 us,
+// 5.0 TB/s.  Sorted rows are read past the caches, which keep what comes next: that
+// alone took there and back together from 160 to 121 us.  A wave a token, so that all
+// rows' first columns were read at once, took 90 us back; zeros by a wave an expert 55 us
+// for any sizes.
 constexpr int kZeroGroups = 64;
 
 // A token's choices from k0 on, at most 64 of them, a lane each: their rows, -1 for none.
@@ -528,6 +534,10 @@ __device__ __forceinline__ TileJob tile_job(const ExpertMatmulArgs& a, unsigned 
   return o;
 }
 
+// Bound as the plain product's tiles are where experts have many rows (16384 x 5632 x
+// 2048: plain 204 us, 8 experts 187 to 191); with many experts also by their
+// weights' way from memory, each of which one round of tiles reads (32764 rows x 2816 x 1024: plain
+// 107 us, 64 experts 157 to 164, of 457 MB).
 template <class C, int FA, int FB, bool F32>
 __global__ __launch_bounds__(C::NT, 2) void expert_tile_kernel(ExpertMatmulArgs a, unsigned tn, bool rest_apart) {
   ExpertLanes lanes;
@@ -550,7 +560,10 @@ __global__ __launch_bounds__(TileSmall::NT, 2) void expert_rest_kernel(ExpertMat
 }
 
 // Few rows an expert: units of 32 rows and 64 columns, 16 a wave, an even share of
-// them to each of as many workgroups as the card holds.  Codes and scales come by
+// them to each of as many workgroups as the card holds.  Bound by memory: 8 experts of
+// 11008 x 4096 (361 MB) and 4 rows each take 65 us, 5.5 TB/s (reads alone reach 6.3 to 7).
+// Straight from memory into registers it took 91 to 105 us, narrow tiles, which wait
+// for each stage's copies before the next, 84 to 93.  Codes and scales come by
 // direct-to-LDS copies into a ring of kStages blocks of 128 of the summed axis, which runs
 // on through the units: what a unit begins with is on its way while the one before
 // it ends.  The weights' codes pass the caches by, as they are read once.
@@ -712,6 +725,9 @@ __device__ __forceinline__ int nth_largest(const ExpertPlan& p, int n) {
 }
 
 // The weights' gradients: every expert's (n, k) tiles, summed over its blocks of 128 rows.
+// Bound by the matrix cores: 32768 rows of 8 uneven experts x 5632 x 2048 in fp32 take
+// 580 to 615 us, 1.23 to 1.3 PFLOP/s (the plain product 1.35; 71 % of a busy CU's cycles
+// issue products).  With each expert's tiles on one XCD it took 1379 us.
 template <class C, int FA, int FB, bool F32>
 __global__ __launch_bounds__(C::NT, 2) void expert_weight_kernel(ExpertMatmulArgs a, unsigned tm, unsigned tn) {
   auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };

@@ -120,6 +120,11 @@ __device__ __forceinline__ int clamp4(int64_t left) { return left >= 4 ? 4 : lef
 
 // A thread's elements, kAdamParts times four of them.  The gradient's type is known here,
 // so that every load is on its way before the first is used.
+// Bound by memory: 103M elements with bf16 gradients and fp32 moments (2.68 GB) take
+// 404 us, 6.6 TB/s; 92M with fp32 gradients and 8-bit moments (1.48 GB) 252 to 263, 5.6
+// to 5.9 (a large copy runs at 4.7 to 5).  Eight neighbouring elements a thread, through the caches,
+// took 469 and 286 us; past the caches that way, in half lines, the second took 393.
+// 1024 or 4096 elements a workgroup take the second to 289 and 285.
 constexpr int kAdamParts = kAdamChunk / 1024;
 template <typename G, bool EIGHT>
 __device__ __forceinline__ void adamw_part(const AdamArgs& a, const AdamTensor& t, int64_t first, float factor) {
@@ -221,6 +226,8 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 // a thread's share of a chunk's squares: its type known, so that four loads are on their way at once
+// (with the type looked up at each load 65 us for 103M bf16 elements, now 37 behind an
+// AdamW step and 57 behind work that fills the last-level cache)
 template <typename G>
 __device__ __forceinline__ double squares(const NormTensor& t, int64_t first) {
   double sum = 0.0;
