@@ -492,10 +492,15 @@ int most_tiles(const ExpertPlan& p, int bm) {
   return static_cast<int>((p.capacity + some * (bm > p.align ? bm - p.align : 0)) / bm);
 }
 
-// workgroup j of n: zeros in c's rows behind the last expert's
+// workgroup j of n: zeros in c's rows behind the last expert's, 16 bytes at a time
 __device__ __forceinline__ void zero_tail(const ExpertMatmulArgs& a, int64_t j, int64_t n) {
+  typedef u16x8 zeros_any __attribute__((aligned(2)));
+  const int size = a.c_dtype == OKLS_F32 ? 4 : 2, per = 16 / size;
   for (int64_t r = min(max(a.plan.offsets[a.plan.n_experts], 0), a.plan.capacity) + j; r < a.plan.capacity; r += n)
-    for (int64_t c = threadIdx.x; c < a.n; c += blockDim.x) store_any(a.c, r * a.ldc + c, a.c_dtype, 0.0f);
+    for (int64_t c = threadIdx.x * per; c < a.n; c += static_cast<int64_t>(blockDim.x) * per) {
+      if (c + per <= a.n) *reinterpret_cast<zeros_any*>(static_cast<uint8_t*>(a.c) + (r * a.ldc + c) * size) = u16x8{};
+      else for (int64_t e = c; e < a.n; ++e) store_any(a.c, r * a.ldc + e, a.c_dtype, 0.0f);
+    }
 }
 
 __device__ __forceinline__ TileJob expert_job(const ExpertMatmulArgs& a, const TileRows& rows) {
