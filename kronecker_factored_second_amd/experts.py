@@ -108,7 +108,12 @@ class Plan:
     offsets (n_experts + 1) int32: each expert's first row, multiples of `align`.
     counts (n_experts) int32: each expert's choices; its other rows hold zeros.
     """
-    __slots__ = ("rows", "pairs", "offsets", "counts", "align", "capacity", "tokens", "each", "n_experts", "device", "_struct", "_address")
+    __slots__ = ("_tensors", "_at", "align", "capacity", "tokens", "each", "n_experts", "device", "_struct", "_address")
+
+    rows = property(lambda self: self._tensors[0])
+    pairs = property(lambda self: self._tensors[1])
+    offsets = property(lambda self: self._tensors[2])
+    counts = property(lambda self: self._tensors[3])
 
     def __init__(self, rows, pairs, offsets, counts, align=128):
         if rows.dim() != 2 or pairs.dim() != 1 or offsets.dim() != 1 or counts.dim() != 1:
@@ -126,15 +131,22 @@ class Plan:
         self._set(rows, pairs, offsets, counts, align, room, tokens, each, n_experts)
 
     def _set(self, rows, pairs, offsets, counts, align, room, tokens, each, n_experts):
-        self.rows, self.pairs, self.offsets, self.counts = rows, pairs, offsets, counts
+        self._tensors = rows, pairs, offsets, counts
+        self._at = rows.data_ptr(), pairs.data_ptr(), offsets.data_ptr(), counts.data_ptr()
         self.align, self.capacity, self.tokens, self.each, self.n_experts, self.device = align, room, tokens, each, n_experts, rows.device
-        self._struct = PlanStruct(rows.data_ptr(), pairs.data_ptr(), offsets.data_ptr(), counts.data_ptr(), tokens, each, room, n_experts, align)
+        self._struct = PlanStruct(*self._at, tokens, each, room, n_experts, align)
         self._address = ctypes.addressof(self._struct)
 
     def address(self):
         """The address of the C view, of the tensors as they lie now."""
-        s = self._struct
-        s.rows, s.pairs, s.offsets, s.counts = self.rows.data_ptr(), self.pairs.data_ptr(), self.offsets.data_ptr(), self.counts.data_ptr()
+        rows, pairs, offsets, counts = self._tensors
+        at = rows.data_ptr(), pairs.data_ptr(), offsets.data_ptr(), counts.data_ptr()
+        if at != self._at:
+            if (rows.numel(), pairs.numel(), offsets.numel(), counts.numel()) != (self.tokens * self.each, self.capacity, self.n_experts + 1, self.n_experts):
+                raise ValueError(f"the plan's tensors changed their sizes: rows {tuple(rows.shape)}, pairs {tuple(pairs.shape)}, "
+                                 f"offsets {tuple(offsets.shape)}, counts {tuple(counts.shape)}")
+            s, self._at = self._struct, at
+            s.rows, s.pairs, s.offsets, s.counts = at
         return self._address
 
 

@@ -208,3 +208,23 @@ def test_stack_dequantizes():
     s.blocked.scales.view(torch.uint8).fill_(127)
     v = s.dequantize()
     assert v.shape == (e, n, k) and torch.equal(v[1, 2], s.blocked.codes[18, :k].float())
+
+
+def test_a_plan_keeps_its_tensors():
+    """A plan's tensors cannot be replaced, and ones that changed their sizes are refused before anything is launched."""
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    room = experts.capacity(4, 2, 3)
+    p = experts.Plan.__new__(experts.Plan)
+    p._set(i32(4, 2), i32(room), i32(4), i32(3), 128, room, 4, 2, 3)
+    struct = experts.PlanStruct.from_address(p.address())
+    assert (struct.rows, struct.pairs, struct.offsets, struct.counts) == tuple(t.data_ptr() for t in (p.rows, p.pairs, p.offsets, p.counts))
+    for name in ("rows", "pairs", "offsets", "counts"):
+        with pytest.raises(AttributeError):
+            setattr(p, name, i32(1))
+    for t in (p.rows, p.pairs, p.offsets, p.counts):
+        kept, n = t.clone(), t.numel()
+        t.set_(i32(n - 1))
+        with pytest.raises(ValueError):
+            p.address()
+        t.set_(kept)
+        assert p.address()
