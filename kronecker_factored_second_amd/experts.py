@@ -416,4 +416,8 @@ def _apply(x, weight, order, grad_dtype, gathered):
         raise ValueError(f"x is {tuple(x.shape)} and weight {tuple(weight.shape)}, the plan has {order.n_experts} experts")
     if order.align != 128 and torch.is_grad_enabled() and weight.requires_grad:
         raise ValueError(f"the weights' gradient needs a plan with align=128, got {order.align}")
-    return _Linear.apply(x, weight, order, grad_dtype, gathered)
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad):
+        return _Linear.apply(x, weight, order, grad_dtype, gathered)
+    # no transposed forms, which only gradients read
+    q, _ = _quantize_rows(x, order, torch.float8_e4m3fn, gathered, True, False)
+    return matmul(q, quantize_stack(weight), order, dtype=x.dtype)

@@ -442,6 +442,20 @@ def test_forward_without_gradients():
             assert torch.equal(experts.combine(ys, w[t: t + 1], one), y[t: t + 1])
 
 
+@pytest.mark.parametrize("gathered", [False, True])
+def test_no_grad_forward_is_the_training_forward(gathered):
+    """Under no_grad nothing is kept for a gradient, and a plan of close rows will do for weights that ask for one elsewhere."""
+    _, choice, _, p = _case(26, 40, 2, 6)
+    rng, close = _rng(27, 40, 6), experts.plan(torch.tensor(choice).cuda(), 6, align=32)
+    x, W = _t(rng.standard_normal((40, 300)), "bf16"), _t(0.1 * rng.standard_normal((6, 200, 300))).requires_grad_()
+    run = lambda order: (experts.token_linear(x, W, order) if gathered else experts.linear(experts.gather(x, order), W, order))  # noqa: E731
+    y = run(p)
+    with torch.no_grad():
+        same, near = run(p), run(close)
+        assert torch.equal(experts.combine(near, None, close), experts.combine(y, None, p))
+    assert y.requires_grad and not same.requires_grad and torch.equal(same, y)
+
+
 def test_refusals():
     _, _, _, p = _case(18, 30, 2, 4)
     _, _, _, close = _case(18, 30, 2, 4, align=16)
