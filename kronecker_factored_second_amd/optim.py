@@ -199,7 +199,9 @@ class AdamW:
     """AdamW over a list of float32 tensors of any shapes, with the interface of
     `okls.OKLS`: .step(), .zero_grad(), .state_dict(), .load_state_dict().  Gradients are
     read from p.grad (float32, bfloat16 or float16) unless `grads` is passed to
-    step().  moments="8bit" holds both moments in 2 bytes a parameter instead of 8."""
+    step().  moments="8bit" holds both moments in 2 bytes a parameter instead of 8.
+    A step that a norm without a finite value holds back counts in .t all the same: the
+    host does not wait to learn of it."""
 
     def __init__(self, params, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, moments="fp32"):
         self.params = list(params)
