@@ -13,7 +13,8 @@ there is no fallback.
     y = linear(act(h), down, order)
     out = combine(y, best.softmax(1), order)                # (tokens, k)
 
-`gather`, `combine`, `linear` and `token_linear` are autograd operators.  To serve,
+`gather`, `combine`, `linear` and `token_linear` are autograd operators, of first
+derivatives backward; forward-mode ones are refused.  To serve,
 keep `quantize_stack(weight)` and call `plan` with align=16, `quantize_rows` and
 `matmul`, which record no gradient.
 """
@@ -22,6 +23,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import linear as _dense
@@ -381,8 +383,16 @@ class _Linear(torch.autograd.Function):
         return dx, dweight, None, None, None
 
 
+def _no_tangents(*tensors):
+    """Refuses forward-mode derivatives, which no operator here has: a tensor that carries a
+    tangent need not require a gradient, and a result without one would count as a constant."""
+    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError("the experts' operators have no forward-mode derivatives")
+
+
 def gather(x, order: Plan):
     """Tokens' rows x (tokens, k) in the sorted order: (order.capacity, k), zeros in rows without a choice."""
+    _no_tangents(x)
     if x.requires_grad and torch.is_grad_enabled():
         return _Gather.apply(x, order)
     return _gather(x, order)
@@ -392,6 +402,7 @@ def combine(y, weights, order: Plan):
     """Each token's sum over its choices of weights (tokens, each) times their rows of
     y (order.capacity, k), in fp32, rounded once: (tokens, k) in y's dtype.  Dropped choices add
     nothing, and what y holds in rows without a choice is not read.  weights=None: ones."""
+    _no_tangents(y, weights)
     if torch.is_grad_enabled() and (y.requires_grad or (weights is not None and weights.requires_grad)):
         return _Combine.apply(y, weights, order)
     return _combine(y, None if weights is None else _weights(weights, order), order)
@@ -412,6 +423,7 @@ def token_linear(x, weight, order: Plan, grad_dtype=torch.float8_e4m3fn):
 
 
 def _apply(x, weight, order, grad_dtype, gathered):
+    _no_tangents(x, weight)
     if weight.dim() != 3 or x.dim() != 2 or weight.shape[0] != order.n_experts or weight.shape[2] != x.shape[1]:
         raise ValueError(f"x is {tuple(x.shape)} and weight {tuple(weight.shape)}, the plan has {order.n_experts} experts")
     if order.align != 128 and torch.is_grad_enabled() and weight.requires_grad:

@@ -228,3 +228,41 @@ def test_a_plan_keeps_its_tensors():
             p.address()
         t.set_(kept)
         assert p.address()
+
+
+# ---------------------------------------------------------------------------
+# Autograd
+# ---------------------------------------------------------------------------
+def _cpu_plan(tokens=4, each=2, n=3):
+    """A plan whose tensors lie on the CPU, for what happens before a launch."""
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    room = experts.capacity(tokens, each, n)
+    p = experts.Plan.__new__(experts.Plan)
+    p._set(i32(tokens, each), i32(room), i32(n + 1), i32(n), 128, room, tokens, each, n)
+    return p
+
+
+def _no_launch(monkeypatch):
+    """Every step that would launch something fails the test instead."""
+    def launched(*args, **kwargs):
+        raise AssertionError("a launch")
+    for name in ("_call", "_gather", "_combine", "_quantize_rows", "_quantize_stack", "matmul"):
+        monkeypatch.setattr(experts, name, launched)
+
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_forward_mode_is_refused(monkeypatch, grad):
+    """A dual tensor does not require a gradient, and a result without a tangent would count as a constant: refused before anything is launched, under no_grad too, which leaves forward mode on."""
+    _no_launch(monkeypatch)
+    p = _cpu_plan()
+    x, xs, w, W = torch.randn(4, 8), torch.randn(p.capacity, 8), torch.rand(4, 2), torch.randn(3, 5, 8)
+    with torch.autograd.forward_ad.dual_level(), torch.set_grad_enabled(grad):
+        dual = lambda t: torch.autograd.forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for bad in (lambda: experts.gather(dual(x), p), lambda: experts.combine(dual(xs), w, p), lambda: experts.combine(xs, dual(w), p),
+                    lambda: experts.combine(dual(xs), None, p), lambda: experts.linear(dual(xs), W, p), lambda: experts.linear(xs, dual(W), p),
+                    lambda: experts.token_linear(dual(x), W, p), lambda: experts.token_linear(x, dual(W), p),
+                    lambda: experts.gather(dual(x).requires_grad_(), p)):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                bad()
+        with pytest.raises(AssertionError, match="a launch"):      # a level alone refuses nothing
+            experts.gather(x, p)
