@@ -109,6 +109,9 @@ class Plan:
     pairs (capacity) int32: the choice t * each + k of each row, -1 for a row without one.
     offsets (n_experts + 1) int32: each expert's first row, multiples of `align`.
     counts (n_experts) int32: each expert's choices; its other rows hold zeros.
+
+    Autograd's operators keep the plan, not copies: what writes into its tensors between a
+    forward and its backward pass makes the second raise.
     """
     __slots__ = ("_tensors", "_at", "align", "capacity", "tokens", "each", "n_experts", "device", "_struct", "_address")
 
@@ -150,6 +153,10 @@ class Plan:
             s, self._at = self._struct, at
             s.rows, s.pairs, s.offsets, s.counts = at
         return self._address
+
+    def _versions(self):
+        """How often torch has written to each tensor in place (inference tensors do not count)."""
+        return [None if t.is_inference() else t._version for t in self._tensors]
 
 
 def plan(choice, n_experts, align=128) -> Plan:
@@ -318,22 +325,34 @@ def weight_grad(a: Blocked, b: Blocked, order: Plan, dtype=torch.float32):
 # --------------------------------------------------------------------------
 # Autograd
 # --------------------------------------------------------------------------
+def _keep(ctx, order):
+    """Keeps the plan for the backward pass.  Not by save_for_backward, which refuses inference tensors: a plan has no gradient."""
+    ctx.order, ctx.versions = order, order._versions()
+
+
+def _kept(ctx):
+    """The forward pass's plan, which must be as it was: its gradients follow the same rows."""
+    if ctx.order._versions() != ctx.versions:
+        raise RuntimeError("the plan was modified in place after the forward pass, whose gradients need it as it was")
+    return ctx.order
+
+
 class _Gather(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, order):
-        ctx.order = order
+        _keep(ctx, order)
         return _gather(x, order)
 
     @staticmethod
     @once_differentiable     # the kernels below have no gradients of their own
     def backward(ctx, dout):
-        return _combine(_rows(dout), None, ctx.order), None
+        return _combine(_rows(dout), None, _kept(ctx)), None
 
 
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, order):
-        ctx.order = order
+        _keep(ctx, order)
         weights = None if weights is None else _weights(weights, order)
         out = _combine(y, weights, order)
         ctx.save_for_backward(*([] if weights is None else [y, weights]))
@@ -342,7 +361,7 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     @once_differentiable     # the kernels below have no gradients of their own
     def backward(ctx, dout):
-        order, dout = ctx.order, _rows(dout)
+        order, dout = _kept(ctx), _rows(dout)
         if not ctx.saved_tensors:
             return _gather(dout, order), None, None
         y, weights = ctx.saved_tensors
@@ -364,14 +383,15 @@ class _Linear(torch.autograd.Function):
         q, t = _quantize_rows(x, order, torch.float8_e4m3fn, gathered, True, need_w)
         w, wt = _quantize_stack(weight, torch.float8_e4m3fn, True, need_x)
         ctx.save_for_backward(*([t.codes, t.scales] if need_w else []), *([wt.blocked.codes, wt.blocked.scales] if need_x else []))
-        ctx.order, ctx.grad_dtype, ctx.gathered, ctx.dtypes, ctx.shape = order, grad_dtype, gathered, (x.dtype, weight.dtype), weight.shape
+        _keep(ctx, order)
+        ctx.grad_dtype, ctx.gathered, ctx.dtypes, ctx.shape = grad_dtype, gathered, (x.dtype, weight.dtype), weight.shape
         return matmul(q, w, order, dtype=x.dtype)
 
     @staticmethod
     @once_differentiable     # the kernels below have no gradients of their own
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad[:2]
-        order, (e, n, k), saved = ctx.order, ctx.shape, ctx.saved_tensors
+        order, (e, n, k), saved = _kept(ctx), ctx.shape, ctx.saved_tensors
         dq, dt = _quantize_rows(_rows(dy), order, ctx.grad_dtype, False, need_x, need_w)
         dx = dweight = None
         if need_w:

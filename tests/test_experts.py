@@ -266,3 +266,49 @@ def test_forward_mode_is_refused(monkeypatch, grad):
                 bad()
         with pytest.raises(AssertionError, match="a launch"):      # a level alone refuses nothing
             experts.gather(x, p)
+
+
+def _stubs(monkeypatch):
+    """The operators' launches as plain tensors of the right sizes on the CPU."""
+    monkeypatch.setattr(experts, "_gather", lambda x, p: x.new_zeros(p.capacity, x.shape[1]))
+    monkeypatch.setattr(experts, "_combine", lambda y, w, p: y.new_zeros(p.tokens, y.shape[1]))
+    monkeypatch.setattr(experts, "_call", lambda *args: None)
+    monkeypatch.setattr(experts, "_matrix", lambda name, t: t.shape[1])
+    monkeypatch.setattr(linear.Blocked, "address", lambda self: 0)
+    monkeypatch.setattr(experts, "_quantize_stack", lambda W, dtype, along, across: (
+        experts.Stack.empty(W.shape, dtype, W.device) if along else None, experts.Stack.empty((W.shape[0], W.shape[2], W.shape[1]), dtype, W.device) if across else None))
+
+
+def _passes(p):
+    """(forward pass of one leaf, the leaf) of every operator, and of combine with and without weights."""
+    x, xs, w, W = torch.randn(4, 8), torch.randn(p.capacity, 8), torch.rand(4, 2), torch.randn(3, 5, 8)
+    for f, leaf in ((lambda t: experts.gather(t, p), x), (lambda t: experts.combine(t, None, p), xs), (lambda t: experts.combine(t, w, p), xs),
+                    (lambda t: experts.combine(xs, t, p), w), (lambda t: experts.linear(t, W, p), xs), (lambda t: experts.linear(xs, t, p), W),
+                    (lambda t: experts.token_linear(t, W, p), x), (lambda t: experts.token_linear(x, t, p), W)):
+        yield f, leaf.clone().requires_grad_()
+
+
+def test_a_plan_written_to_between_the_passes_is_noticed(monkeypatch):
+    """Gradients follow the forward pass's rows: a plan whose tensors torch wrote to in between makes the backward pass raise, one that is as it was does not."""
+    _stubs(monkeypatch)
+    for name in ("rows", "pairs", "offsets", "counts"):
+        p = _cpu_plan()
+        for f, leaf in _passes(p):
+            f(leaf).sum().backward()
+            assert leaf.grad.shape == leaf.shape
+            y = f(leaf).sum()
+            getattr(p, name).zero_()
+            with pytest.raises(RuntimeError, match="modified in place"):
+                y.backward()
+            f(leaf).sum().backward()        # a pass after the write has its own
+
+
+def test_a_plan_of_inference_tensors_trains(monkeypatch):
+    """A plan made under inference_mode has no count of writes, and autograd refuses to save its tensors: the operators take it all the same."""
+    _stubs(monkeypatch)
+    with torch.inference_mode():
+        p = _cpu_plan()
+    assert p.rows.is_inference()
+    for f, leaf in _passes(p):
+        f(leaf).sum().backward()
+        assert leaf.grad.shape == leaf.shape
