@@ -446,6 +446,12 @@ def _apply(x, weight, order, grad_dtype, gathered):
     _no_tangents(x, weight)
     if weight.dim() != 3 or x.dim() != 2 or weight.shape[0] != order.n_experts or weight.shape[2] != x.shape[1]:
         raise ValueError(f"x is {tuple(x.shape)} and weight {tuple(weight.shape)}, the plan has {order.n_experts} experts")
+    # all of it before the first launch, and what only the backward pass uses too
+    _sorted("x", x, order, order.tokens if gathered else order.capacity)
+    if weight.dtype not in DTYPES or weight.device != order.device:
+        raise ValueError(f"weight must be float32, bfloat16 or float16 on {order.device}, got {weight.dtype} on {weight.device}")
+    if grad_dtype not in _dense.FORMATS:
+        raise ValueError(f"grad_dtype must be float8_e4m3fn or float8_e5m2, got {grad_dtype}")
     if order.align != 128 and torch.is_grad_enabled() and weight.requires_grad:
         raise ValueError(f"the weights' gradient needs a plan with align=128, got {order.align}")
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad):

@@ -312,3 +312,21 @@ def test_a_plan_of_inference_tensors_trains(monkeypatch):
     for f, leaf in _passes(p):
         f(leaf).sum().backward()
         assert leaf.grad.shape == leaf.shape
+
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_a_layer_refuses_before_anything_is_launched(monkeypatch, grad):
+    """Wrong types and devices of the weight and the gradient's 8-bit type, which only the backward pass uses, as well."""
+    _no_launch(monkeypatch)
+    monkeypatch.setattr(experts, "_matrix", lambda name, t: t.shape[1])
+    p = _cpu_plan()
+    x, xs, W = torch.randn(4, 8).requires_grad_(grad), torch.randn(p.capacity, 8).requires_grad_(grad), torch.randn(3, 5, 8)
+    for W_bad, kw in ((W.double(), {}), (W.to("meta"), {}), (W.long(), {}), (W, dict(grad_dtype=torch.float16)), (W, dict(grad_dtype=None)), (W, dict(grad_dtype=torch.float8_e8m0fnu))):
+        for run, rows in ((experts.token_linear, x), (experts.linear, xs)):
+            with pytest.raises(ValueError):
+                run(rows, W_bad, p, **kw)
+    for run, rows in ((experts.token_linear, xs), (experts.linear, x), (experts.linear, xs.detach().to("meta"))):
+        with pytest.raises(ValueError):
+            run(rows, W, p)
+    with pytest.raises(AssertionError, match="a launch"):
+        experts.linear(xs, W, p, grad_dtype=torch.float8_e5m2)
