@@ -36,11 +36,6 @@ __device__ __forceinline__ void for_each(F&& f) {
   }
 }
 
-__device__ __forceinline__ intx8 frag(const uint8_t* p) {
-  const intx4 lo = reinterpret_cast<const intx4*>(p)[0], hi = reinterpret_cast<const intx4*>(p)[1];
-  return intx8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-}
-
 // codes 8 s .. 8 s + 7 of a lane's, times 2^(byte - 127), in bf16
 template <int F, class V>
 __device__ __forceinline__ bf16x8 widen(const V& f, int s, int byte) {
@@ -405,105 +400,6 @@ __device__ __forceinline__ void tile_product(const TileJob& o) {
   WAIT_VM(0);              // the last copies land before the buffers are used again or given up
   if constexpr (C::NW == 8) barrier();
   finish();
-}
-
-// Bound by memory: one row through 11008 x 4096 (45 MB) takes 11.4 us, 4.0 TB/s
-// with the launch in it.
-// Few rows of a (16 TM of them a workgroup): c's columns in groups of 16 TN a workgroup,
-// whose waves split the summed axis in turn and add up through LDS.  Every code
-// of b is read once and straight into registers, U blocks of 128 a wave at a time.
-constexpr int kFewWaves = 8;
-template <int TM, int TN, int FA, int FB, bool F32>
-__device__ __forceinline__ void few_product(const TileJob& o) {
-  constexpr int U = TM + TN <= 3 ? 4 : 2;        // blocks of k a wave has in flight
-  __shared__ floatx4 part[kFewWaves][TM * TN][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m = o.m, n = o.n, m0 = o.m0, n0 = o.n0, blocks = o.nst;
-  int64_t ra[TM], rb[TN];
-  const uint8_t *pa[TM], *pb[TN];
-  // rows past the end read the last one; what they give is not stored
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int64_t r = m0 + 16 * i + (lane & 15);
-    ra[i] = r < m ? r : m - 1;
-    pa[i] = o.a_codes + ra[i] * o.lda + (lane >> 4) * 32;
-  }
-#pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const int64_t r = n0 + 16 * j + (lane & 15);
-    rb[j] = r < n ? r : n - 1;
-    pb[j] = o.b_codes + rb[j] * o.ldb + (lane >> 4) * 32;
-  }
-  floatx4 acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = floatx4{};
-  auto run = [&](int64_t k, auto uc) {
-    constexpr int nu = decltype(uc)::value;
-    intx8 fa[nu][TM], fb[nu][TN];
-    int sa[nu][TM], sb[nu][TN];
-#pragma unroll
-    for (int u = 0; u < nu; ++u) {
-      const int64_t kb = k + u * kFewWaves;
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        fb[u][j] = frag(pb[j] + kb * 128);
-        sb[u][j] = o.b_scales[kb * o.ldb_scale + rb[j]];
-      }
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        fa[u][i] = frag(pa[i] + kb * 128);
-        sa[u][i] = o.a_scales[kb * o.lda_scale + ra[i]];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < nu; ++u) {
-      if constexpr (F32) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          bf16x8 wb[TN];
-#pragma unroll
-          for (int j = 0; j < TN; ++j) wb[j] = widen<FB>(fb[u][j], s, sb[u][j]);
-#pragma unroll
-          for (int i = 0; i < TM; ++i) {
-            const bf16x8 wa = widen<FA>(fa[u][i], s, sa[u][i]);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], wa, acc[i][j], 0, 0, 0);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[u][j], fa[u][i], acc[i][j], FB, FA, 0, sb[u][j], 0, sa[u][i]);
-      }
-    }
-  };
-  int64_t k = wave;
-  for (; k + (U - 1) * kFewWaves < blocks; k += U * kFewWaves) run(k, std::integral_constant<int, U>{});
-  for (; k < blocks; k += kFewWaves) run(k, std::integral_constant<int, 1>{});
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) part[wave][i * TN + j][lane] = acc[i][j];
-  __syncthreads();
-  // lane l of a block holds c[l % 16][4 (l / 16) + e]
-  for (int t = threadIdx.x; t < TM * TN * 64; t += kFewWaves * 64) {
-    const int blk = t >> 6, l = t & 63;
-    floatx4 s = part[0][blk][l];
-#pragma unroll
-    for (int q = 1; q < kFewWaves; ++q) s += part[q][blk][l];
-    const int64_t row = m0 + blk / TN * 16 + (l & 15), col = n0 + blk % TN * 16 + (l >> 4) * 4;
-    if (row >= m) continue;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (col + e < n) {
-        const int64_t at = row * o.ldc + col + e;
-        store_any(o.c, at, o.c_dtype, o.accumulate ? s[e] + load_any(o.c, at, o.c_dtype) : s[e]);
-      }
-  }
 }
 
 // calls go(a's format, b's format, fp32 result) with compile-time values
