@@ -1,9 +1,16 @@
 // gfx950 kernels of the experts' operators (okls_experts.h).
 //
-//  plan_kernel and its parts   a stable counting sort of choices by expert.
-//  gather / combine kernels    tokens' rows to the sorted order and back.
-//  expert tile / few kernels   the products of product_tile.h, each tile of the
-//                              sorted rows with its own expert's matrix.
+//  plan_one_kernel       a stable counting sort of choices by expert in one workgroup;
+//  plan_rank_kernel,     in several, ranks within each one's choices,
+//  plan_place_kernel     then rows from all workgroups' counts.
+//  gather_kernel         tokens' rows to the sorted order;
+//  combine_kernel        back, weighted and summed: also the gradient of the first;
+//  combine_backward_kernel   the gradients of the second.
+//  expert_stream_kernel  the product where experts have few rows, through a ring in LDS.
+//  expert_tile_kernel    the product by product_tile.h's tiles, each with its own
+//                        expert's matrix; expert_rest_kernel, what whole rounds of
+//                        large tiles leave over.
+//  expert_weight_kernel  the weights' gradients, by the same tiles.
 #include "experts_kernels.h"
 #include "product_tile.h"
 
@@ -761,10 +768,6 @@ __global__ __launch_bounds__(C::NT, 2) void expert_weight_kernel(ExpertMatmulArg
   tile_product<C, FA, FB, F32>(o);
 }
 
-__global__ __launch_bounds__(256) void zero_matrix_kernel(void* c, int dtype, int64_t m, int64_t n, int64_t ldc) {
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < m * n; i += gridDim.x * 256ll) store_any(c, i / n * ldc + i % n, dtype, 0.0f);
-}
-
 int bits_of(int n_experts) {
   int b = 0;
   while (1 << b <= n_experts) ++b;      // numbers up to n_experts itself: none
@@ -854,7 +857,7 @@ hipError_t launch_combine_backward(const RowsArgs& a, hipStream_t s) {
 //    98 / 80.
 hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s) {
   if (a.a.cols == 0) {
-    zero_matrix_kernel<<<blocks_up_to((a.plan.capacity * a.n + 255) / 256, 4096), 256, 0, s>>>(a.c, a.c_dtype, a.plan.capacity, a.n, a.ldc);
+    zero_kernel<<<blocks_up_to((a.plan.capacity * a.n + 255) / 256, 4096), 256, 0, s>>>(a.c, a.c_dtype, a.plan.capacity, a.n, a.ldc);
     return hipGetLastError();
   }
   const ExpertPlan& p = a.plan;

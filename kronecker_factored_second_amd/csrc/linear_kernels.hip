@@ -576,10 +576,6 @@ __global__ __launch_bounds__(kFewWaves * 64) void matmul_few_kernel(MatmulArgs a
   }
 }
 
-__global__ __launch_bounds__(256) void zero_kernel(void* c, int dtype, int64_t m, int64_t n, int64_t ldc) {
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < m * n; i += gridDim.x * 256ll) store_any(c, i / n * ldc + i % n, dtype, 0.0f);
-}
-
 }  // namespace
 
 hipError_t launch_quantize(const QuantArgs& a, hipStream_t s) {

@@ -402,6 +402,11 @@ __device__ __forceinline__ void tile_product(const TileJob& o) {
   finish();
 }
 
+// a product with nothing to sum
+__global__ __launch_bounds__(256) void zero_kernel(void* c, int dtype, int64_t m, int64_t n, int64_t ldc) {
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < m * n; i += gridDim.x * 256ll) store_any(c, i / n * ldc + i % n, dtype, 0.0f);
+}
+
 // calls go(a's format, b's format, fp32 result) with compile-time values
 template <class F>
 void by_format(int32_t format_a, int32_t format_b, int32_t c_dtype, F go) {
