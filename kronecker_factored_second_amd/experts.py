@@ -113,7 +113,7 @@ class Plan:
     Autograd's operators keep the plan, not copies: what writes into its tensors between a
     forward and its backward pass makes the second raise.
     """
-    __slots__ = ("_tensors", "_at", "align", "capacity", "tokens", "each", "n_experts", "device", "_struct", "_address")
+    __slots__ = ("_tensors", "_counted", "_at", "align", "capacity", "tokens", "each", "n_experts", "device", "_struct", "_address")
 
     rows = property(lambda self: self._tensors[0])
     pairs = property(lambda self: self._tensors[1])
@@ -137,6 +137,7 @@ class Plan:
 
     def _set(self, rows, pairs, offsets, counts, align, room, tokens, each, n_experts):
         self._tensors = rows, pairs, offsets, counts
+        self._counted = [t for t in self._tensors if not t.is_inference()]       # those hold no count of writes
         self._at = rows.data_ptr(), pairs.data_ptr(), offsets.data_ptr(), counts.data_ptr()
         self.align, self.capacity, self.tokens, self.each, self.n_experts, self.device = align, room, tokens, each, n_experts, rows.device
         self._struct = PlanStruct(*self._at, tokens, each, room, n_experts, align)
@@ -155,8 +156,8 @@ class Plan:
         return self._address
 
     def _versions(self):
-        """How often torch has written to each tensor in place (inference tensors do not count)."""
-        return [None if t.is_inference() else t._version for t in self._tensors]
+        """How often torch has written to each tensor in place."""
+        return [t._version for t in self._counted]
 
 
 def plan(choice, n_experts, align=128) -> Plan:
