@@ -95,6 +95,35 @@ def test_decay_without_gradients():
     assert A.hold(np.full(128, nearest), np.full(128, 0.5), True)[0][0] * A.hold(np.full(128, nearest), np.full(128, 0.5), True)[1][0] == 1.0
 
 
+def test_roots_far_below_their_block_stay():
+    """A root below the smallest normal code (2^-6 of 448, 3.5e-5 of its block's largest) always rounds up: while the largest stays where it is, so does the small one, and does not fall as 0.999^t makes the formula's."""
+    start = np.full(128, 2e-5)
+    start[0] = 1.0
+    m, s = (np.zeros(128), np.ones(1)), A.hold(start, np.full(128, 0.5), True)
+    first = A.held(*s)[1:]
+    g = np.zeros(128)
+    g[0] = 1.0
+    for t in range(1, 301):
+        _, m, s = A.step8(np.zeros(128), g, m, s, t, 0, lr=0.0, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0)
+    assert A.held(*s)[0] == 1.0 and np.array_equal(A.held(*s)[1:], first) and (first >= 2e-5).all() and (first < 2e-5 + 2.0 ** -17).all()
+
+
+def test_roots_scatter_in_steady_state():
+    """Gradients of one size each.  A step moves the root s by 0.0005 s |z^2 - 1|, 0.968 of 0.0005 s on average, and rounds with a variance of that times a code's step, 0.0902 s on average over the logarithm from s / 16 to s / 8: 4.37e-5 s^2.  What is off falls by a thousandth a step, so the variance settles at 4.37e-5 / 0.002 and the deviation at 0.148.  The drift, 0.0005 (v / s - s), is zero on average where the mean of 1 / s, (1 + 0.022) over s's, is s's over v: a mean of 1.011, and of the square 1.044.  2000 steps reach 0.98 of the variance.  1024 elements give the deviation within 0.148 / 45 and the means within 0.148 / 32 and twice that; v's own deviation, 1.6 % of the root, moves s with it for the most part."""
+    rng = np.random.default_rng(3)
+    n, hyper = 1024, dict(lr=0.0, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0)
+    size = np.exp(rng.standard_normal(n))
+    m, s, v = (np.zeros(n), np.ones(n // 128)), A.hold(size, np.full(n, 0.5), True), size ** 2
+    for t in range(1000, 3000):
+        g = size * rng.standard_normal(n)
+        _, m, s = A.step8(np.zeros(n), g, m, s, t, 0, **hyper)
+        v = 0.999 * v + 0.001 * g * g
+    ratio = A.held(*s) / np.sqrt(v)
+    assert abs(ratio.std() - 0.148) < 5 * 0.148 / 45 + 0.01 * 0.148 + 0.0016      # five deviations; the variance's last 2 %; a tenth of v's own
+    assert abs(ratio.mean() - 1.011) < 5 * 0.148 / 32
+    assert abs((ratio ** 2).mean() - 1.044) < 5 * 2 * 0.148 / 32
+
+
 def test_thresholds_are_spread():
     """65536 elements: a mean of 1/2 within 5 of its standard deviations (0.289 / 256), different for steps and places, and the element's upper 32 bits count."""
     u, w = A.thresholds(3, 1, 65536)
