@@ -13,8 +13,9 @@
  * of rows holds two experts.  The sizes of all tensors follow from numbers that
  * the host knows: `capacity` rows are enough for any choices, and the host never
  * waits to learn them.  Rows without a choice, up to the capacity, are zeros in
- * everything written here, except that an expert's weights that are not finite give
- * NaN in its own.
+ * everything written here, except that a product's come from its operand's, which are zeros
+ * if okls_experts_quantize_rows made it, and that an expert's weights that are not
+ * finite give NaN in its own.
  *
  * Conventions, as in okls_linear.h: device pointers on the current device,
  * row-major with a free row stride, the caller owns every tensor and the
@@ -90,13 +91,15 @@ okls_status okls_experts_quantize_stack(const void* x, int32_t dtype, int32_t n_
                                         const okls_blocked* along_rows, void* stream);
 
 /* c[r] = a[r] b_e^T for the rows r of each expert e: a (capacity x k) and the stack b
- * (n_experts up(n, 16) x k) in 8 bits, c (capacity, n) of c_dtype.  Sums as in
- * okls_scaled_matmul. */
+ * (n_experts up(n, 16) x k) in 8 bits, c (capacity, n) of c_dtype; zeros behind the last
+ * expert's rows.  An expert's rows without a choice are multiplied like its others
+ * (okls_experts_quantize_rows makes them zeros).  Sums as in okls_scaled_matmul. */
 okls_status okls_experts_matmul(const okls_expert_plan* plan, const okls_blocked* a, const okls_blocked* b, int64_t n,
                                 void* c, int32_t c_dtype, int64_t ldc, void* stream);
 
 /* c_e = sum over the rows r of expert e of a[:, r] b[:, r]^T, zeros for an
- * expert without rows: a (n x capacity) and b (k x capacity) in 8 bits, c
+ * expert without rows; rows without a choice are summed too, as zeros from
+ * okls_experts_quantize_rows.  a (n x capacity) and b (k x capacity) in 8 bits, c
  * (n_experts, n, k) of c_dtype with row stride ldc, matrices n ldc apart.  The
  * plan's align must be 128. */
 okls_status okls_experts_weight_grad(const okls_expert_plan* plan, const okls_blocked* a, const okls_blocked* b,

@@ -573,8 +573,9 @@ __global__ __launch_bounds__(TileSmall::NT, 2) void expert_rest_kernel(ExpertMat
 
 // Few rows an expert: units of 32 rows and 64 columns, 16 a wave, an even share of
 // them to each of as many workgroups as the card holds.  Bound by memory: 8 experts of
-// 11008 x 4096 (361 MB) and 4 rows each take 65 us, 5.5 TB/s (reads alone reach 6.3 to 7).
-// Straight from memory into registers it took 91 to 105 us, narrow tiles, which wait
+// 11008 x 4096 (364 MB) and 4 rows each take 75 to 77 us with four sets of weights in
+// turn, 4.8 TB/s (reads alone reach 6.3 to 7); with one set, half of which the
+// last-level cache may serve, 61 to 76 from card to card.  With one set, straight from memory into registers it took 91 to 105 us, narrow tiles, which wait
 // for each stage's copies before the next, 84 to 93.  Codes and scales come by
 // direct-to-LDS copies into a ring of kStages blocks of 128 of the summed axis, which runs
 // on through the units: what a unit begins with is on its way while the one before

@@ -290,7 +290,10 @@ def _quantize_stack(weight, dtype, along, across):
 
 def matmul(a: Blocked, b: Stack, order: Plan, dtype=torch.bfloat16):
     """Rows r of each expert e of a (capacity, k) times b_e^T: (capacity, n) of
-    `dtype`, zeros in rows without a choice.  Sums as `linear.matmul` sums `dtype`."""
+    `dtype`, zeros behind the last expert's rows.  An expert's rows without a choice are
+    multiplied like its others: zeros from `quantize_rows`' zeros, where the expert's
+    weights are finite.  Sums as `linear.matmul` sums `dtype`: a 16-bit result drops, from
+    each eight products, what lies below 2^-13 of the largest of them."""
     e, n, k = b.shape
     pa, pb, device = a.address(), b.blocked.address(), a.codes.device
     if a.shape != (order.capacity, k) or e != order.n_experts:
@@ -307,7 +310,8 @@ def matmul(a: Blocked, b: Stack, order: Plan, dtype=torch.bfloat16):
 def weight_grad(a: Blocked, b: Blocked, order: Plan, dtype=torch.float32):
     """(n_experts, n, k) of `dtype`: for each expert a[:, rows] b[:, rows]^T over its
     rows, for the transposed forms a (n, capacity) and b (k, capacity); zeros for an
-    expert without rows.  The plan's align must be 128."""
+    expert without rows.  Its rows without a choice are summed too: `quantize_rows` makes
+    them zeros.  The plan's align must be 128."""
     pa, pb, device = a.address(), b.address(), a.codes.device
     (n, ra), (k, rb) = a.shape, b.shape
     if ra != order.capacity or rb != order.capacity:
@@ -431,15 +435,16 @@ def combine(y, weights, order: Plan):
 
 def linear(x, weight, order: Plan, grad_dtype=torch.float8_e4m3fn):
     """Sorted rows x (order.capacity, k) through their experts' matrices, weight
-    (n_experts, n, k): (order.capacity, n) in x's dtype, zeros in rows without a choice.
-    Products and gradients as `linear.scaled_linear`'s; weight's gradient needs a plan
+    (n_experts, n, k): (order.capacity, n) in x's dtype, zeros in rows without a choice
+    of an expert whose weights are finite.  Products and gradients as `linear.scaled_linear`'s; weight's gradient needs a plan
     with align=128 and is zeros for an expert without tokens."""
     return _apply(x, weight, order, grad_dtype, False)
 
 
 def token_linear(x, weight, order: Plan, grad_dtype=torch.float8_e4m3fn):
     """`linear` of gather(x): the tokens x (tokens, k) are brought to 8 bits straight
-    into the sorted order, and x's gradient is the sum over its choices."""
+    into the sorted order, and x's gradient is the sum over its choices, each rounded to
+    x's dtype before the fp32 sum, as `gather`'s gradient would be."""
     return _apply(x, weight, order, grad_dtype, True)
 
 

@@ -629,3 +629,46 @@ def test_example_runs():
     for a, b in zip(got, want):
         # products of two rounded factors, two layers deep, and the output's gradient in two bits of fraction
         assert (a.double().cpu() - b).norm() < 2.0 ** -2 * b.norm()
+
+
+def test_forward_mode_is_refused():
+    """With a tangent nothing comes back; without one, the same calls under a dual level do."""
+    rng, _, _, p = _case(28, 30, 2, 4)
+    x, W, w = _t(rng.standard_normal((30, 40))), _t(rng.standard_normal((4, 24, 40))), _t(rng.random((30, 2)))
+    want = experts.combine(experts.token_linear(x, W, p), w, p)
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual
+        for bad in (lambda: experts.gather(dual(x, x), p), lambda: experts.token_linear(x, dual(W, W), p), lambda: experts.combine(experts.token_linear(x, W, p), dual(w, w), p)):
+            with pytest.raises(NotImplementedError):
+                bad()
+        assert torch.equal(experts.combine(experts.token_linear(x, W, p), w, p), want)
+
+
+def test_a_plan_written_to_between_the_passes():
+    """The backward pass of a plan over buffers that were filled again raises; a pass of its own on them gives their gradients."""
+    _, _, _, a = _case(29, 60, 2, 5)
+    _, _, _, b = _case(30, 60, 2, 5)
+    held = experts.Plan(*[getattr(a, n).clone() for n in ("rows", "pairs", "offsets", "counts")])
+    x, dxs = torch.randn(60, 72, device="cuda").requires_grad_(), torch.randn(a.capacity, 72, device="cuda")
+    want = [torch.autograd.grad(experts.gather(x, p), x, dxs)[0] for p in (a, b)]
+    assert torch.equal(torch.autograd.grad(experts.gather(x, held), x, dxs)[0], want[0])
+    y = experts.gather(x, held)
+    for n in ("rows", "pairs", "offsets", "counts"):
+        getattr(held, n).copy_(getattr(b, n))
+    with pytest.raises(RuntimeError, match="modified in place"):
+        torch.autograd.grad(y, x, dxs)
+    assert torch.equal(torch.autograd.grad(experts.gather(x, held), x, dxs)[0], want[1])
+
+
+@pytest.mark.parametrize("tokens,each,e,n", [(9, 2, 5, 70), (150, 2, 7, 300), (1000, 2, 8, 4000)])
+def test_rows_without_a_choice_multiply_as_they_are(tokens, each, e, n):
+    """An operand of one's own may hold anything in an expert's rows without a choice; behind the last expert's rows there are zeros whatever it holds."""
+    rng, choice, (_, pairs, offsets, _), p = _case(31, tokens, each, e)
+    a = linear.quantize(_t(rng.standard_normal((p.capacity, 200))))
+    b = experts.quantize_stack(_t(0.1 * rng.standard_normal((e, n, 200))))
+    c = experts.matmul(a, b, p, dtype=torch.float32)
+    A, B = _held(a), _n(b.dequantize())
+    for i in range(e):
+        rows = slice(int(offsets[i]), int(offsets[i + 1]))
+        _check_sums(c[rows], A[rows] @ B[i].T, np.abs(A[rows]) @ np.abs(B[i]).T, 200, "f32")
+    assert not c[int(offsets[-1]):].any()
