@@ -35,6 +35,7 @@ EXPORTED = ("okls_experts_capacity", "okls_experts_plan_workspace_size", "okls_e
             "okls_experts_quantize_stack", "okls_experts_matmul", "okls_experts_weight_grad")
 MAX_EXPERTS = 512
 ALIGNS = (16, 32, 64, 128)
+MAX_SUMMED = (1 << 24) - 128    # of a product's axis: its rows of codes lie less than 2^24 bytes apart
 
 
 class PlanStruct(ctypes.Structure):
@@ -458,6 +459,10 @@ def _apply(x, weight, order, grad_dtype, gathered):
         raise ValueError(f"weight must be float32, bfloat16 or float16 on {order.device}, got {weight.dtype} on {weight.device}")
     if grad_dtype not in _dense.FORMATS:
         raise ValueError(f"grad_dtype must be float8_e4m3fn or float8_e5m2, got {grad_dtype}")
+    # summed over: the rows' columns, and in gradients the result's columns and the sorted rows
+    grad, (_, n, k) = torch.is_grad_enabled(), weight.shape
+    if max(k, n if grad and x.requires_grad else 0, order.capacity if grad and weight.requires_grad else 0) > MAX_SUMMED:
+        raise ValueError(f"products sum over at most {MAX_SUMMED}, got k = {k}, n = {n} and {order.capacity} sorted rows")
     if order.align != 128 and torch.is_grad_enabled() and weight.requires_grad:
         raise ValueError(f"the weights' gradient needs a plan with align=128, got {order.align}")
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad):

@@ -330,3 +330,26 @@ def test_a_layer_refuses_before_anything_is_launched(monkeypatch, grad):
             run(rows, W, p)
     with pytest.raises(AssertionError, match="a launch"):
         experts.linear(xs, W, p, grad_dtype=torch.float8_e5m2)
+
+
+def test_a_layer_refuses_sums_that_only_its_gradients_cannot_take(monkeypatch):
+    """Rows of codes 2^24 bytes apart are refused by the products, those of the gradients too: here before the forward pass, and only where a gradient needs them."""
+    _no_launch(monkeypatch)
+    monkeypatch.setattr(experts, "_matrix", lambda name, t: t.shape[1])
+    meta = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device="meta")  # noqa: E731
+    i32 = lambda *s: meta(*s, dtype=torch.int32)  # noqa: E731
+
+    def runs(tokens, n, k, need_x, need_w):
+        room = experts.capacity(tokens, 1, 2)
+        p = experts.Plan.__new__(experts.Plan)
+        p._set(i32(tokens, 1), i32(room), i32(3), i32(2), 128, room, tokens, 1, 2)
+        with pytest.raises((ValueError, AssertionError)) as e:
+            experts.token_linear(meta(tokens, k).requires_grad_(need_x), meta(2, n, k).requires_grad_(need_w), p)
+        return e.type is AssertionError         # it went on to a launch
+    most = (1 << 24) - 128
+    assert experts.MAX_SUMMED == most
+    fits = most - 2 * 127           # tokens of whose choices any leave at most `most` rows
+    for need_x, need_w in ((False, False), (True, False), (False, True), (True, True)):
+        assert runs(4, 8, most, need_x, need_w) and not runs(4, 8, most + 1, need_x, need_w)
+        assert runs(4, most, 8, need_x, need_w) and runs(4, most + 1, 8, need_x, need_w) == (not need_x)
+        assert runs(fits, 8, 8, need_x, need_w) and runs(1 << 24, 8, 8, need_x, need_w) == (not need_w)
