@@ -331,6 +331,13 @@ def weight_grad(a: Blocked, b: Blocked, order: Plan, dtype=torch.float32):
 # --------------------------------------------------------------------------
 # Autograd
 # --------------------------------------------------------------------------
+def _no_tangents(*tensors):
+    """Refuses forward-mode derivatives, which no operator here has: a tensor that carries a
+    tangent need not require a gradient, and a result without one would count as a constant."""
+    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError("the experts' operators have no forward-mode derivatives")
+
+
 def _keep(ctx, order):
     """Keeps the plan for the backward pass.  Not by save_for_backward, which refuses inference tensors: a plan has no gradient."""
     ctx.order, ctx.versions = order, order._versions()
@@ -352,6 +359,7 @@ class _Gather(torch.autograd.Function):
     @staticmethod
     @once_differentiable     # the kernels below have no gradients of their own
     def backward(ctx, dout):
+        _no_tangents(dout)
         return _combine(_rows(dout), None, _kept(ctx)), None
 
 
@@ -367,6 +375,7 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     @once_differentiable     # the kernels below have no gradients of their own
     def backward(ctx, dout):
+        _no_tangents(dout)
         order, dout = _kept(ctx), _rows(dout)
         if not ctx.saved_tensors:
             return _gather(dout, order), None, None
@@ -396,6 +405,7 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     @once_differentiable     # the kernels below have no gradients of their own
     def backward(ctx, dy):
+        _no_tangents(dy)
         need_x, need_w = ctx.needs_input_grad[:2]
         order, (e, n, k), saved = _kept(ctx), ctx.shape, ctx.saved_tensors
         dq, dt = _quantize_rows(_rows(dy), order, ctx.grad_dtype, False, need_x, need_w)
@@ -407,13 +417,6 @@ class _Linear(torch.autograd.Function):
             if ctx.gathered:
                 dx = _combine(dx, None, order)
         return dx, dweight, None, None, None
-
-
-def _no_tangents(*tensors):
-    """Refuses forward-mode derivatives, which no operator here has: a tensor that carries a
-    tangent need not require a gradient, and a result without one would count as a constant."""
-    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
-        raise NotImplementedError("the experts' operators have no forward-mode derivatives")
 
 
 def gather(x, order: Plan):

@@ -353,3 +353,15 @@ def test_a_layer_refuses_sums_that_only_its_gradients_cannot_take(monkeypatch):
         assert runs(4, 8, most, need_x, need_w) and not runs(4, 8, most + 1, need_x, need_w)
         assert runs(4, most, 8, need_x, need_w) and runs(4, most + 1, 8, need_x, need_w) == (not need_x)
         assert runs(fits, 8, 8, need_x, need_w) and runs(1 << 24, 8, 8, need_x, need_w) == (not need_w)
+
+
+def test_a_gradient_with_a_tangent_is_refused(monkeypatch):
+    """Forward mode over a backward pass: the gradient that comes in carries a tangent, and what goes on would carry none."""
+    _stubs(monkeypatch)
+    for f, leaf in _passes(_cpu_plan()):
+        with torch.autograd.forward_ad.dual_level():
+            y = f(leaf)
+            d = torch.autograd.forward_ad.make_dual(torch.ones_like(y), torch.ones_like(y))
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                torch.autograd.grad(y, leaf, d)
+            assert torch.autograd.grad(f(leaf), leaf, torch.ones_like(y))[0].shape == leaf.shape
