@@ -23,12 +23,11 @@ from __future__ import annotations
 import ctypes
 
 import torch
-from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import linear as _dense
 from . import okls
-from .linear import Blocked, BlockedStruct, DTYPES, _matrix, _rows, _up
+from .linear import Blocked, BlockedStruct, DTYPES, _matrix, _no_tangents, _rows, _up
 
 EXPORTED = ("okls_experts_capacity", "okls_experts_plan_workspace_size", "okls_experts_plan", "okls_experts_gather",
             "okls_experts_combine", "okls_experts_combine_backward", "okls_experts_quantize_rows",
@@ -331,13 +330,6 @@ def weight_grad(a: Blocked, b: Blocked, order: Plan, dtype=torch.float32):
 # --------------------------------------------------------------------------
 # Autograd
 # --------------------------------------------------------------------------
-def _no_tangents(*tensors):
-    """Refuses forward-mode derivatives, which no operator here has: a tensor that carries a
-    tangent need not require a gradient, and a result without one would count as a constant."""
-    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
-        raise NotImplementedError("the experts' operators have no forward-mode derivatives")
-
-
 def _keep(ctx, order):
     """Keeps the plan for the backward pass.  Not by save_for_backward, which refuses inference tensors: a plan has no gradient."""
     ctx.order, ctx.versions = order, order._versions()

@@ -27,6 +27,7 @@ import operator
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import okls
@@ -339,6 +340,13 @@ def rms_norm_backward(dy, h, rstd, weight, dh=None):
 # --------------------------------------------------------------------------
 # Autograd
 # --------------------------------------------------------------------------
+def _no_tangents(*tensors):
+    """Refuses forward-mode derivatives, which no operator of the library has: a tensor that carries
+    a tangent need not require a gradient, and a result without one would count as a constant."""
+    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError("this operator has no forward-mode derivative")
+
+
 class _NormLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, norm_weight, weight, eps, grad_dtype):
@@ -357,6 +365,7 @@ class _NormLinear(torch.autograd.Function):
         need_x, need_r, need_n, need_w = ctx.needs_input_grad[:4]
         if dy is None:      # only the residual stream went on
             return dh if need_x else None, dh if need_r else None, None, None, None, None
+        _no_tangents(dy, dh)
         dy = _rows(dy)
         dx = dnorm = dweight = None
         if need_w:
@@ -385,6 +394,7 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     @once_differentiable     # the kernels below have no gradients of their own
     def backward(ctx, dy):
+        _no_tangents(dy)
         need_x, need_w = ctx.needs_input_grad[:2]
         saved = ctx.saved_tensors
         kept = [Blocked(saved[2 * i], saved[2 * i + 1], s) for i, s in enumerate(ctx.shapes)]

@@ -274,3 +274,25 @@ def test_blocked_view_follows_its_tensors():
         q.struct()
     with pytest.raises(ValueError, match="GPU"):
         q.address()
+
+
+def test_a_gradient_with_a_tangent_is_refused(monkeypatch):
+    """Forward mode over a backward pass: an incoming gradient's tangent would be lost in the layers' gradients; only the residual stream hands it on as it is."""
+    one = lambda t, transpose=False, **kw: linear.Blocked.empty(*(t.T if transpose else t).shape, torch.float8_e4m3fn, "cpu")  # noqa: E731
+    monkeypatch.setattr(linear, "quantize", one)
+    monkeypatch.setattr(linear, "quantize_both", lambda t, **kw: (one(t), one(t.T)))
+    monkeypatch.setattr(linear, "rms_norm", lambda x, w, residual=None, eps=0: linear.NormOutput(one(x), x if residual is None else x + residual, x[:, 0]))
+    monkeypatch.setattr(linear, "rms_norm_backward", lambda dv, h, rstd, w, dh=None: (torch.zeros_like(h), torch.zeros_like(w)))
+    monkeypatch.setattr(linear, "matmul", lambda a, b, dtype: torch.zeros(a.shape[0], b.shape[0], dtype=dtype))
+    x, r, w, W = (torch.randn(*s).requires_grad_() for s in ((4, 8), (4, 8), (8,), (5, 8)))
+    dual = torch.autograd.forward_ad.make_dual
+    with torch.autograd.forward_ad.dual_level():
+        for outs, leaves in (((linear.scaled_linear(x, W),), (x, W)), (linear.rms_norm_linear(x, w, W)[:1], (x, w, W)), (linear.rms_norm_linear(x, w, W, residual=r), (x, r, w, W))):
+            ones = [torch.ones_like(o) for o in outs]
+            for i, o in enumerate(ones):
+                with pytest.raises(NotImplementedError, match="forward-mode"):
+                    torch.autograd.grad(outs, leaves, [dual(d, d) if j == i else d for j, d in enumerate(ones)], retain_graph=True)
+            assert all(g.shape == t.shape for g, t in zip(torch.autograd.grad(outs, leaves, ones, retain_graph=True), leaves))
+        h, d = outs[1], dual(torch.ones(4, 8), torch.full((4, 8), 2.0))
+        for g in torch.autograd.grad(h, (x, r), d):
+            assert torch.equal(torch.autograd.forward_ad.unpack_dual(g).tangent, torch.full((4, 8), 2.0))
