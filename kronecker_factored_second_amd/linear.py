@@ -15,8 +15,8 @@ the HIP library on the current stream, and there is no fallback.
                 dtype=torch.float32)                        # the optimizer's G
     dx, dnorm = rms_norm_backward(dv, h, rstd, norm_weight, dh=dh)
 
-`rms_norm_linear` and `scaled_linear` are these calls as autograd operators.  The
-single calls record nothing: their results carry no gradient back to inputs that
+`rms_norm_linear` and `scaled_linear` are these calls as autograd operators, of
+first derivatives backward; forward-mode ones are refused.  The single calls record nothing: their results carry no gradient back to inputs that
 require one.
 """
 from __future__ import annotations
