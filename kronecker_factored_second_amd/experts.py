@@ -110,8 +110,9 @@ class Plan:
     offsets (n_experts + 1) int32: each expert's first row, multiples of `align`.
     counts (n_experts) int32: each expert's choices; its other rows hold zeros.
 
-    Autograd's operators keep the plan, not copies: what writes into its tensors between a
-    forward and its backward pass makes the second raise.
+    Autograd's operators keep the plan, not copies: a torch operation that writes into its
+    tensors between a forward and its backward pass makes the second raise.  A captured
+    graph's replay is not seen: its plan belongs to that graph's own backward pass.
     """
     __slots__ = ("_tensors", "_counted", "_at", "align", "capacity", "tokens", "each", "n_experts", "device", "_struct", "_address")
 
@@ -432,8 +433,9 @@ def combine(y, weights, order: Plan):
 def linear(x, weight, order: Plan, grad_dtype=torch.float8_e4m3fn):
     """Sorted rows x (order.capacity, k) through their experts' matrices, weight
     (n_experts, n, k): (order.capacity, n) in x's dtype, zeros in rows without a choice
-    of an expert whose weights are finite.  Products and gradients as `linear.scaled_linear`'s; weight's gradient needs a plan
-    with align=128 and is zeros for an expert without tokens."""
+    of an expert whose weights are finite.  Products and gradients as
+    `linear.scaled_linear`'s; weight's gradient needs a plan with align=128 and is zeros
+    for an expert without tokens."""
     return _apply(x, weight, order, grad_dtype, False)
 
 
